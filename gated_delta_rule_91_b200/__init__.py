@@ -17,6 +17,13 @@ Functions (same names as the C entry points):
     gdr_block_epilogue(o, g, weight, eps)                 -> y
     gdr_block_epilogue_bwd(o, g, weight, dy, eps)         -> (do, dg, dweight)
     gdr_seg_fwd / gdr_seg_combine / gdr_seg_fixup         (sequence split; see seq_split)
+    gdr_ssm_fwd(x, delta, A, Bm, Cm, D, delta_bias, S0)   -> (y, S_T)   (selective state space scan)
+    gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, dy, dS_T) -> dict of gradients
+    gdr_ssm_step(x, delta, A, Bm, Cm, S, D, delta_bias)   -> y  (S advanced in place)
+    gdr_conv_fwd(x, w, bias, ...)                         -> y  (short causal convolution)
+    gdr_conv_bwd(x, w, dy, bias, ...)                     -> dict of gradients
+    gdr_layernorm_fwd(x, weight, bias, residual, eps)     -> (y, h)
+    gdr_layernorm_bwd(h, weight, dy, dres, eps)           -> (dx, dweight, dbias)
 
 The calls take the current CUDA stream and allocate nothing inside the
 library, so they can be captured in CUDA graphs.  `autograd` wraps the
@@ -60,6 +67,17 @@ SIGNATURES = {
     "gdr_seg_fwd_workspace_bytes": (_SZ, [_I] * 6),
     "gdr_seg_combine": (_I, [_I] * 6 + [_P] * 5 + [_P]),
     "gdr_seg_fixup": (_I, [_I] * 6 + [_P] * 3 + [_P]),
+    "gdr_ssm_fwd": (_I, [_I] * 8 + [_P, _I, _P, _P, _P, _I, _P, _I] + [_P] * 5 + [_P, _SZ, _P]),
+    "gdr_ssm_fwd_workspace_bytes": (_SZ, [_I] * 7),
+    "gdr_ssm_bwd": (_I, [_I] * 8 + [_P, _I, _P, _P, _P, _I, _P, _I] + [_P] * 13 + [_P, _SZ, _P]),
+    "gdr_ssm_bwd_workspace_bytes": (_SZ, [_I] * 7),
+    "gdr_ssm_step": (_I, [_I] * 7 + [_P, _I, _P, _P, _P, _I, _P, _I] + [_P] * 4 + [_P]),
+    "gdr_conv_fwd": (_I, [_I] * 6 + [_P, _I] + [_P] * 5 + [_P]),
+    "gdr_conv_bwd": (_I, [_I] * 6 + [_P, _I] + [_P] * 9 + [_P, _SZ, _P]),
+    "gdr_conv_bwd_workspace_bytes": (_SZ, [_I] * 4),
+    "gdr_layernorm_fwd": (_I, [ctypes.c_int64, _I, _I] + [_P] * 4 + [ctypes.c_float] + [_P] * 2 + [_P]),
+    "gdr_layernorm_bwd": (_I, [ctypes.c_int64, _I, _I] + [_P] * 2 + [ctypes.c_float] + [_P] * 5 + [_P, _SZ, _P]),
+    "gdr_layernorm_bwd_workspace_bytes": (_SZ, [_I]),
     "gdr_check_status": (_I, [_P]),
     "gdr_debug_wait_timeout": (_I, [_I, _P]),
     "gdr_last_error_string": (ctypes.c_char_p, []),
@@ -364,3 +382,236 @@ def gdr_seg_fixup(qt, S_in, o):
     _f32(S_in, "S_in")
     check(lib().gdr_seg_fixup(B, T, H, dk, dv, _dt(qt), _ptr(qt), _ptr(S_in), _ptr(o), _stream(qt)))
     return o
+
+
+def _like(name, t, shape, dtype, device):
+    """`t` (None passes) as a dense operand of this shape, type and device; returns its address."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device or not t.is_cuda:
+        raise ValueError("%s must be on the CUDA device of the other tensors (%s), got %s" % (name, device, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, lead, dtype, device):
+    """`t` as rows of a wider buffer: the axes from `lead` on are a dense row, and the rows of the leading axes are
+    one stride apart.  Returns (address, stride in elements)."""
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device or not t.is_cuda:
+        raise ValueError("%s must be on the CUDA device of the other tensors (%s), got %s" % (name, device, t.device))
+    strides = t.stride()
+    width = 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] > 1 and strides[i] != width:
+            raise ValueError("%s: the axes of a row must be contiguous" % name)
+        width *= shape[i]
+    ld, rows = 0, 1
+    for i in range(lead - 1, -1, -1):
+        if shape[i] > 1:
+            if rows == 1:
+                ld = strides[i]
+                if ld < width:
+                    raise ValueError("%s: rows must not overlap (stride %d, width %d)" % (name, ld, width))
+            elif strides[i] != rows * ld:
+                raise ValueError("%s: the rows of all batches must be one stride apart" % name)
+            rows *= shape[i]
+    return t.data_ptr(), ld or width
+
+
+class _on:
+    """Makes the tensors' device current around a call (launches go to the current device)."""
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def _cuda(x, name):
+    if not x.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % name)
+    return x.device
+
+
+def _out(name, t, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else t
+
+
+def _scratch(nbytes, device, workspace):
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the tensors' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, lead):
+    """Sizes, type and addresses of the scan's inputs; lead = 2: [B,T,...], 1: [B,...]."""
+    dev, dt = _cuda(x, "x"), _dt(x)
+    if x.dim() != lead + 2 or Bm.dim() != lead + 2:
+        raise ValueError("x and Bm must have %d axes, got %s and %s" % (lead + 2, tuple(x.shape), tuple(Bm.shape)))
+    H, P = x.shape[-2:]
+    G, N = Bm.shape[-2:]
+    rows = x.shape[:lead]
+    px, ldx = _rows("x", x, x.shape, lead, x.dtype, dev)
+    pb, ldb = _rows("Bm", Bm, rows + (G, N), lead, x.dtype, dev)
+    pc, ldc = _rows("Cm", Cm, rows + (G, N), lead, x.dtype, dev)
+    f = torch.float32
+    pd = _like("delta", delta, rows + (H,), f, dev)
+    pA = _like("A", A, (H,), f, dev)
+    pD = _like("D", D, (H,), f, dev)
+    pbias = _like("delta_bias", delta_bias, (H,), f, dev)
+    return rows, H, G, P, N, dt, dev, (px, ldx, pd, pA, pb, ldb, pc, ldc, pD, pbias)
+
+
+def gdr_ssm_fwd(x, delta, A, Bm, Cm, D=None, delta_bias=None, S0=None, *, softplus=False, y=None, S_T=None,
+                return_state=True, workspace=None):
+    """Selective state space scan: S_t = exp(A Delta_t) S_{t-1} + Delta_t x_t B_t^T, y_t = S_t C_t + D x_t, with
+    Delta = softplus(delta + delta_bias) or delta + delta_bias.  x [B,T,H,P]; Bm, Cm [B,T,G,N] (H/G heads share a
+    group); all three may be slices of one [B,T,channels] buffer.  delta [B,T,H], A, D, delta_bias [H] fp32; S0
+    [B,H,P,N] fp32.  Returns (y, S_T or None)."""
+    (B, T), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 2)
+    y = _out("y", y, (B, T, H, P), x.dtype, dev)
+    if S_T is None and return_state:
+        S_T = torch.empty(B, H, P, N, dtype=torch.float32, device=dev)
+    f = torch.float32
+    L = lib()
+    ws, ws_bytes = _scratch(L.gdr_ssm_fwd_workspace_bytes(B, T, H, G, P, N, dt), dev, workspace)
+    with _on(dev):
+        check(L.gdr_ssm_fwd(B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev),
+                            _like("y", y, (B, T, H, P), x.dtype, dev), _like("S_T", S_T, (B, H, P, N), f, dev),
+                            ws.data_ptr(), ws_bytes, torch.cuda.current_stream(dev).cuda_stream))
+    return y, S_T
+
+
+def gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, dy, dS_T=None, *, softplus=False, want_dS0=True,
+                workspace=None):
+    """Backward of gdr_ssm_fwd.  Returns dict(dx, ddelta, dA, dB, dC, dD, ddelta_bias, dS0); dD and ddelta_bias are
+    None without D and delta_bias."""
+    (B, T), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 2)
+    f = torch.float32
+    e = lambda *shape, dtype=f: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+    out = dict(dx=e(B, T, H, P, dtype=x.dtype), ddelta=e(B, T, H), dA=e(H), dB=e(B, T, G, N, dtype=x.dtype),
+               dC=e(B, T, G, N, dtype=x.dtype), dD=None if D is None else e(H),
+               ddelta_bias=None if delta_bias is None else e(H), dS0=e(B, H, P, N) if want_dS0 else None)
+    L = lib()
+    ws, ws_bytes = _scratch(L.gdr_ssm_bwd_workspace_bytes(B, T, H, G, P, N, dt), dev, workspace)
+    with _on(dev):
+        check(L.gdr_ssm_bwd(B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev),
+                            _like("dy", dy, (B, T, H, P), x.dtype, dev), _like("dS_T", dS_T, (B, H, P, N), f, dev),
+                            *(None if t is None else t.data_ptr() for t in out.values()), ws.data_ptr(), ws_bytes,
+                            torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+def gdr_ssm_step(x, delta, A, Bm, Cm, S, D=None, delta_bias=None, *, softplus=False, y=None):
+    """One token of gdr_ssm_fwd: x [B,H,P]; Bm, Cm [B,G,N]; delta [B,H]; S [B,H,P,N] fp32 advanced in place.
+    Returns y [B,H,P]."""
+    (B,), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 1)
+    y = _out("y", y, (B, H, P), x.dtype, dev)
+    if S is None:
+        raise ValueError("S is required")
+    with _on(dev):
+        check(lib().gdr_ssm_step(B, H, G, P, N, dt, int(softplus), *ptrs,
+                                 _like("S", S, (B, H, P, N), torch.float32, dev),
+                                 _like("y", y, (B, H, P), x.dtype, dev),
+                                 torch.cuda.current_stream(dev).cuda_stream))
+    return y
+
+
+def _conv_operands(x, w, bias, conv_state):
+    dev, dt = _cuda(x, "x"), _dt(x)
+    if x.dim() != 3 or w.dim() != 2:
+        raise ValueError("x must be [B,T,C] and w [C,K], got %s and %s" % (tuple(x.shape), tuple(w.shape)))
+    B, T, C = x.shape
+    K = w.shape[1]
+    px, ldx = _rows("x", x, x.shape, 2, x.dtype, dev)
+    return (B, T, C, K, dt, dev, (px, ldx, _like("w", w, (C, K), torch.float32, dev),
+                                  _like("bias", bias, (C,), torch.float32, dev),
+                                  _like("conv_state", conv_state, (B, max(K - 1, 0), C), x.dtype, dev)))
+
+
+def gdr_conv_fwd(x, w, bias=None, *, conv_state=None, conv_state_out=None, silu=True, y=None):
+    """Depthwise causal convolution of width K with SiLU: x [B,T,C] (rows of a wider buffer are read in place), w
+    [C,K] and bias [C] fp32.  conv_state [B,K-1,C] (dtype of x) carries the inputs before token 0; conv_state_out
+    receives the last K-1 inputs and may be conv_state itself.  A decode token is T = 1.  Returns y [B,T,C]."""
+    B, T, C, K, dt, dev, ptrs = _conv_operands(x, w, bias, conv_state)
+    y = _out("y", y, (B, T, C), x.dtype, dev)
+    with _on(dev):
+        check(lib().gdr_conv_fwd(B, T, C, K, dt, int(silu), *ptrs,
+                                 _like("conv_state_out", conv_state_out, (B, max(K - 1, 0), C), x.dtype, dev),
+                                 _like("y", y, (B, T, C), x.dtype, dev), torch.cuda.current_stream(dev).cuda_stream))
+    return y
+
+
+def gdr_conv_bwd(x, w, dy, bias=None, *, conv_state=None, dconv_state_out=None, silu=True, want_dbias=None,
+                 want_dconv_state=None, workspace=None):
+    """Backward of gdr_conv_fwd.  Returns dict(dx, dw, dbias (None unless a bias was given or want_dbias),
+    dconv_state (None unless conv_state was given or want_dconv_state))."""
+    B, T, C, K, dt, dev, ptrs = _conv_operands(x, w, bias, conv_state)
+    f = torch.float32
+    want_db = (bias is not None) if want_dbias is None else want_dbias
+    want_ds = (conv_state is not None) if want_dconv_state is None else want_dconv_state
+    out = dict(dx=torch.empty(B, T, C, dtype=x.dtype, device=dev), dw=torch.empty(C, K, dtype=f, device=dev),
+               dbias=torch.empty(C, dtype=f, device=dev) if want_db else None,
+               dconv_state=torch.empty(B, max(K - 1, 0), C, dtype=x.dtype, device=dev) if want_ds else None)
+    L = lib()
+    ws, ws_bytes = _scratch(L.gdr_conv_bwd_workspace_bytes(B, T, C, K), dev, workspace)
+    with _on(dev):
+        check(L.gdr_conv_bwd(B, T, C, K, dt, int(silu), *ptrs, _like("dy", dy, (B, T, C), x.dtype, dev),
+                             _like("dconv_state_out", dconv_state_out, (B, max(K - 1, 0), C), x.dtype, dev),
+                             *(None if t is None else t.data_ptr() for t in out.values()), ws.data_ptr(), ws_bytes,
+                             torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+def gdr_layernorm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, h=None):
+    """Layer norm of h = x + residual over the last axis (x [...,D]; weight, bias [D] fp32).  Returns (y, h); h is
+    None without a residual."""
+    dev, dt, D = _cuda(x, "x"), _dt(x), x.shape[-1]
+    y = _out("y", y, x.shape, x.dtype, dev)
+    if residual is not None and h is None:
+        h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    f = torch.float32
+    with _on(dev):
+        check(lib().gdr_layernorm_fwd(x.numel() // max(D, 1), D, dt, _like("x", x, x.shape, x.dtype, dev),
+                                      _like("residual", residual, x.shape, x.dtype, dev),
+                                      _like("weight", weight, (D,), f, dev), _like("bias", bias, (D,), f, dev),
+                                      float(eps), _like("y", y, x.shape, x.dtype, dev),
+                                      _like("h", h, x.shape, x.dtype, dev),
+                                      torch.cuda.current_stream(dev).cuda_stream))
+    return y, h
+
+
+def gdr_layernorm_bwd(h, weight, dy, *, dres=None, eps=1e-5, want_dbias=True, workspace=None):
+    """Backward of gdr_layernorm_fwd from the stored stream h (x without a residual) and the gradient dres that
+    reaches h along the residual stream.  Returns (dx, dweight, dbias or None)."""
+    dev, dt, D = _cuda(h, "h"), _dt(h), h.shape[-1]
+    f = torch.float32
+    dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+    dweight = torch.empty(D, dtype=f, device=dev)
+    dbias = torch.empty(D, dtype=f, device=dev) if want_dbias else None
+    L = lib()
+    ws, ws_bytes = _scratch(L.gdr_layernorm_bwd_workspace_bytes(D), dev, workspace)
+    with _on(dev):
+        check(L.gdr_layernorm_bwd(h.numel() // max(D, 1), D, dt, _like("h", h, h.shape, h.dtype, dev),
+                                  _like("weight", weight, (D,), f, dev), float(eps),
+                                  _like("dy", dy, h.shape, h.dtype, dev), _like("dres", dres, h.shape, h.dtype, dev),
+                                  dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
+                                  ws.data_ptr(), ws_bytes, torch.cuda.current_stream(dev).cuda_stream))
+    return dx, dweight, dbias

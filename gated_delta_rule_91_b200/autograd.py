@@ -9,12 +9,15 @@ forward's states itself, so nothing else is kept).  Unused outputs arrive as
 zero gradients.  `block_prologue(...)` (ShortConv, SiLU, q/k L2) and
 `block_epilogue(o, g, weight, eps)` (RMSNorm, weight, SiLU gate) are the
 block's steps around the recurrence, differentiated through
-gdr_block_prologue_bwd and gdr_block_epilogue_bwd.
+gdr_block_prologue_bwd and gdr_block_epilogue_bwd.  `selective_scan(x, delta, A,
+Bm, Cm, ...)`, `short_conv(x, w, ...)` and `layer_norm(x, weight, ...)` wrap
+gdr_ssm_fwd, gdr_conv_fwd and gdr_layernorm_fwd with their backwards.
 """
 import torch
 
 from . import (gdr2_bwd, gdr2_fwd, gdr_block_epilogue, gdr_block_epilogue_bwd, gdr_block_prologue,
-               gdr_block_prologue_bwd, gdr_bwd, gdr_fwd)
+               gdr_block_prologue_bwd, gdr_bwd, gdr_conv_bwd, gdr_conv_fwd, gdr_fwd, gdr_layernorm_bwd,
+               gdr_layernorm_fwd, gdr_ssm_bwd, gdr_ssm_fwd)
 
 
 def _c(x):
@@ -112,3 +115,94 @@ class BlockPrologue(torch.autograd.Function):
 def block_prologue(xq, xk, xv, wq, wk, wv, bq=None, bk=None, bv=None, conv_state=None, eps=1e-6):
     """Differentiable gdr_block_prologue: returns (q, k, v)."""
     return BlockPrologue.apply(xq, xk, xv, wq, wk, wv, bq, bk, bv, conv_state, eps)
+
+
+def _dense_rows(x, lead):
+    """x itself where the library reads it in place (rows of a wider buffer), a dense copy otherwise."""
+    if x.is_contiguous():
+        return x
+    shape, strides, width = x.shape, x.stride(), 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] > 1 and strides[i] != width:
+            return x.contiguous()
+        width *= shape[i]
+    ld, rows = 0, 1
+    for i in range(lead - 1, -1, -1):
+        if shape[i] > 1:
+            if (rows == 1 and strides[i] < width) or (rows > 1 and strides[i] != rows * ld):
+                return x.contiguous()
+            ld = strides[i] if rows == 1 else ld
+            rows *= shape[i]
+    per16 = 16 // x.element_size()
+    return x if ld % per16 == 0 and x.data_ptr() % 16 == 0 else x.contiguous()
+
+
+class SelectiveScan(torch.autograd.Function):
+    """S_t = exp(A Delta_t) S_{t-1} + Delta_t x_t B_t^T, y_t = S_t C_t + D x_t."""
+
+    @staticmethod
+    def forward(ctx, x, delta, A, Bm, Cm, D, delta_bias, S0, softplus):
+        x, Bm, Cm = (_dense_rows(t, 2) for t in (x, Bm, Cm))
+        delta, S0 = _c(delta), _c(S0)
+        ctx.softplus = softplus
+        ctx.save_for_backward(x, delta, A, Bm, Cm, D, delta_bias, S0)
+        return gdr_ssm_fwd(x, delta, A, Bm, Cm, D, delta_bias, S0, softplus=softplus)
+
+    @staticmethod
+    def backward(ctx, dy, dS_T):
+        x, delta, A, Bm, Cm, D, delta_bias, S0 = ctx.saved_tensors
+        g = gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, _c(dy), _c(dS_T), softplus=ctx.softplus,
+                        want_dS0=S0 is not None)
+        return g["dx"], g["ddelta"], g["dA"], g["dB"], g["dC"], g["dD"], g["ddelta_bias"], g["dS0"], None
+
+
+def selective_scan(x, delta, A, Bm, Cm, D=None, delta_bias=None, S0=None, softplus=False):
+    """Differentiable gdr_ssm_fwd: returns (y, S_T)."""
+    return SelectiveScan.apply(x, delta, A, Bm, Cm, D, delta_bias, S0, softplus)
+
+
+class ShortConv(torch.autograd.Function):
+    """y = SiLU(bias + causal depthwise convolution of x), the window before token 0 from conv_state."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, conv_state, silu):
+        x, conv_state = _dense_rows(x, 2), _c(conv_state)
+        ctx.silu = silu
+        ctx.save_for_backward(x, w, bias, conv_state)
+        return gdr_conv_fwd(x, w, bias, conv_state=conv_state, silu=silu)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, bias, conv_state = ctx.saved_tensors
+        g = gdr_conv_bwd(x, w, _c(dy), bias, conv_state=conv_state, silu=ctx.silu)
+        return g["dx"], g["dw"], g["dbias"], g["dconv_state"], None
+
+
+def short_conv(x, w, bias=None, conv_state=None, silu=True):
+    """Differentiable gdr_conv_fwd: returns y."""
+    return ShortConv.apply(x, w, bias, conv_state, silu)
+
+
+class LayerNorm(torch.autograd.Function):
+    """y = LN(h) weight + bias with h = x + residual; h is returned for the next block's residual."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        x, residual = _c(x), _c(residual)
+        y, h = gdr_layernorm_fwd(x, weight, bias, residual=residual, eps=eps)
+        ctx.eps, ctx.has_bias, ctx.has_residual = eps, bias is not None, residual is not None
+        ctx.save_for_backward(x if h is None else h, weight)
+        return y, h
+
+    @staticmethod
+    def backward(ctx, dy, dh):
+        h, weight = ctx.saved_tensors
+        dx, dweight, dbias = gdr_layernorm_bwd(h, weight, _c(dy), dres=_c(dh) if ctx.has_residual else None, eps=ctx.eps,
+                                               want_dbias=ctx.has_bias)
+        return dx, dweight, dbias, dx if ctx.has_residual else None, None
+
+
+def layer_norm(x, weight, bias=None, residual=None, eps=1e-5):
+    """Differentiable gdr_layernorm_fwd: returns y, or (y, h) with a residual."""
+    y, h = LayerNorm.apply(x, weight, bias, residual, eps)
+    return y if residual is None else (y, h)

@@ -1,8 +1,8 @@
 // gdr_lib.cu -- the C ABI of libgdr.so (declared in include/gdr.h): argument
 // validation, workspace sizing, kernel selection and the device status word.
-// Every kernel header is included here so the library is one translation
-// unit (the device status word is then a single symbol).
-#include <stdarg.h>
+// Every kernel header of the gated delta rule is included here; the selective
+// scan, the short convolution and the layer norm are in ssm_lib.cu, with a
+// status word of their own that gdr_check_status reads too.
 #include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
@@ -10,6 +10,7 @@
 #include <mutex>
 #include <string>
 
+#include "abi_common.cuh"
 #include "common.cuh"
 #include "step_kernel.cuh"
 #include "fwd_simt.cuh"
@@ -31,37 +32,6 @@ std::atomic<uint64_t> g_launches{0};
 using namespace gdr;
 
 namespace {
-
-thread_local std::string t_last_error;
-
-gdr_status fail(gdr_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
-gdr_status fail(gdr_status s, const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    t_last_error = buf;
-    return s;
-}
-
-gdr_status cuda_fail(cudaError_t e, const char *where) {
-    return fail(GDR_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-#define GDR_REQUIRE_PTR(p)                                                                   \
-    do {                                                                                     \
-        if ((p) == nullptr) return fail(GDR_ERR_INVALID_ARGUMENT, "%s: %s is NULL", fn, #p); \
-        if (!aligned16(p))                                                                   \
-            return fail(GDR_ERR_INVALID_ARGUMENT, "%s: %s is not 16-byte aligned", fn, #p);  \
-    } while (0)
-#define GDR_OPTIONAL_PTR(p)                                                                 \
-    do {                                                                                    \
-        if ((p) != nullptr && !aligned16(p))                                                \
-            return fail(GDR_ERR_INVALID_ARGUMENT, "%s: %s is not 16-byte aligned", fn, #p); \
-    } while (0)
 
 gdr_status check_dims(const char *fn, int B, int T, int H, int dk, int dv, gdr_dtype dt) {
     if (B < 1 || T < 1 || H < 1 || dk < 1 || dv < 1)
@@ -124,9 +94,15 @@ gdr_status gdr_check_status(gdr_stream_t stream) {
     int host = 0, zero = 0;
     e = cudaMemcpyFromSymbol(&host, g_status, sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e, "gdr_check_status: read status");
+    int scan = 0;
+    e = ssm_take_status(&scan);
+    if (e != cudaSuccess) return cuda_fail(e, "gdr_check_status: scan status");
     if (host != 0) {
         e = cudaMemcpyToSymbol(g_status, &zero, sizeof(int));
         if (e != cudaSuccess) return cuda_fail(e, "gdr_check_status: clear status");
+    }
+    if (host == 0) host = scan;
+    if (host != 0) {
         return fail((gdr_status)host, "device status %d: %s", host,
                     host == GDR_ERR_TIMEOUT ? "a bounded on-chip wait gave up"
                                             : "a kernel reported an input it does not handle");

@@ -42,8 +42,8 @@
  *  * A launch failure returns GDR_ERR_CUDA.  Kernels that wait on on-chip
  *    barriers give up after a bounded number of polls and record
  *    GDR_ERR_TIMEOUT in a device status word, read by gdr_check_status().
- *  * Outputs must not alias inputs (except S in gdr_step and gdr2_step, o in gdr_seg_fixup
- *    and the conv state in gdr_block_prologue, which are in-out).
+ *  * Outputs must not alias inputs (except S in gdr_step, gdr2_step and gdr_ssm_step, o in
+ *    gdr_seg_fixup and the conv state in gdr_block_prologue and gdr_conv_fwd, which are in-out).
  *  * gdr_last_error_string() describes the last non-OK status returned on the
  *    calling thread.
  */
@@ -400,6 +400,136 @@ GDR_API gdr_status gdr_seg_combine(int R, int r, int B, int H, int dk, int dv,
  *   in/out: o [B,T,H,dv] (gdr_seg_fwd's o0 on entry).  Sizes as gdr_fwd. */
 GDR_API gdr_status gdr_seg_fixup(int B, int T, int H, int dk, int dv, gdr_dtype dt,
                          const void *qt, const float *S_in, void *o, gdr_stream_t stream);
+
+/*
+ * Selective state space scan: the gated recurrence without the erase, next to
+ * gdr_fwd.  Per batch b and head h, with z_t = delta_t + delta_bias_h and
+ * Delta_t = softplus(z_t) (softplus != 0) or z_t:
+ *     a_t = exp(A_h Delta_t),   S_t = a_t S_{t-1} + Delta_t x_t B_t^T,
+ *     y_t = S_t C_t + D_h x_t            (readout after the update)
+ * x_t has P channels, the state is P x N, and the H/G consecutive heads of a
+ * group share B and C.
+ *   in : x [B,T,H,P], Bm, Cm [B,T,G,N] (dtype dt) with token strides ldx, ldb,
+ *        ldc in elements (0 = dense): token t of batch b starts at row b*T + t,
+ *        so slices of one [B,T,channels] buffer are read in place.  A stride
+ *        is at least the row's width and a multiple of 16 bytes.
+ *        delta [B,T,H], A, D, delta_bias [H] fp32; D and delta_bias may be
+ *        NULL (no skip, no bias).  S0 [B,H,P,N] fp32 or NULL (zero).
+ *   out: y [B,T,H,P] (dtype dt); S_T [B,H,P,N] fp32, or NULL to skip.
+ *   A token with Delta_t = 0 (z_t = -inf under softplus) leaves the state as
+ *   it is: a batch of unequal prompts is padded with such tokens (on the left
+ *   if the convolution's window goes on from its end).  Inputs are finite
+ *   (delta may be -inf); a value that is not spoils the outputs of its chunk of
+ *   128 tokens and of what follows.
+ *   Supported: P, N in {64, 128}; H a multiple of G; B*T*H*max(P,N) < 2^31;
+ *   B, H <= 65535 where T > 1.  workspace: gdr_ssm_fwd_workspace_bytes(...)
+ *   bytes; NULL or short -> GDR_ERR_WORKSPACE.  Repeated calls give the same bits.
+ */
+GDR_API gdr_status gdr_ssm_fwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, int softplus,
+                       const void *x, int ldx, const float *delta, const float *A,
+                       const void *Bm, int ldb, const void *Cm, int ldc,
+                       const float *D, const float *delta_bias, const float *S0,
+                       void *y, float *S_T, void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+GDR_API size_t gdr_ssm_fwd_workspace_bytes(int B, int T, int H, int G, int P, int N, gdr_dtype dt);
+
+/*
+ * Backward of gdr_ssm_fwd.  With G_t the gradient of S_t,
+ *     G_t = dy_t C_t^T + a_{t+1} G_{t+1}   (from dS_T),   dlog_t = a_t <G_t, S_{t-1}>:
+ *     dx = Delta_t G_t B_t + D dy_t,   dB_t = sum_h Delta_t G_t^T x_t,   dC_t = sum_h S_t^T dy_t,
+ *     ddelta_t = (x_t . G_t B_t + A dlog_t) sigmoid(z_t)  (without the sigmoid where softplus = 0),
+ *     dA = sum_{b,t} Delta_t dlog_t,  ddelta_bias = sum_{b,t} ddelta_t,  dD = sum_{b,t} dy_t . x_t,
+ *     dS0 = a_1 G_1.
+ *   in : the forward's inputs; dy [B,T,H,P] (dtype dt, dense); dS_T [B,H,P,N] fp32 or NULL (zero).
+ *   out: dx [B,T,H,P], dB, dC [B,T,G,N] (dtype dt, dense); ddelta [B,T,H],
+ *        dA, dD, ddelta_bias [H], dS0 [B,H,P,N] fp32; dD, ddelta_bias and dS0
+ *        may be NULL (not written).  All are overwritten.
+ *   The states are recomputed from the inputs (nothing of the forward is kept).
+ *   workspace: gdr_ssm_bwd_workspace_bytes(...) bytes.  Errors as gdr_ssm_fwd.
+ */
+GDR_API gdr_status gdr_ssm_bwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, int softplus,
+                       const void *x, int ldx, const float *delta, const float *A,
+                       const void *Bm, int ldb, const void *Cm, int ldc,
+                       const float *D, const float *delta_bias, const float *S0,
+                       const void *dy, const float *dS_T,
+                       void *dx, float *ddelta, float *dA, void *dB, void *dC, float *dD,
+                       float *ddelta_bias, float *dS0,
+                       void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+GDR_API size_t gdr_ssm_bwd_workspace_bytes(int B, int T, int H, int G, int P, int N, gdr_dtype dt);
+
+/*
+ * One token of gdr_ssm_fwd, the state updated in place.
+ *   in : x [B,H,P], Bm, Cm [B,G,N] (dtype dt) with batch strides ldx, ldb, ldc
+ *        (0 = dense); delta [B,H]; A, D, delta_bias as gdr_ssm_fwd.
+ *   in/out: S [B,H,P,N] fp32.   out: y [B,H,P] (dtype dt).
+ */
+GDR_API gdr_status gdr_ssm_step(int B, int H, int G, int P, int N, gdr_dtype dt, int softplus,
+                        const void *x, int ldx, const float *delta, const float *A,
+                        const void *Bm, int ldb, const void *Cm, int ldc,
+                        const float *D, const float *delta_bias, float *S, void *y, gdr_stream_t stream);
+
+/*
+ * Short causal convolution, depthwise over C channels (the scan's x, B and C
+ * side by side, for instance), in the convention of gdr_block_prologue:
+ *     z[t,c] = bias[c] + sum_{j<K} w[c,j] x[t-K+1+j, c],   y = SiLU(z), or z where silu = 0
+ *   in : x [B,T,C] (dtype dt), token stride ldx >= C elements (0 = dense);
+ *        w [C,K], bias [C] fp32 (bias may be NULL); conv_state_in [B,K-1,C]
+ *        (dtype dt): the K-1 inputs before token 0, oldest first; NULL = zeros.
+ *   out: y [B,T,C] (dtype dt); conv_state_out (layout of conv_state_in, may be
+ *        NULL): the last K-1 inputs, for the next segment or token.  It may
+ *        equal conv_state_in.  A decode token is the call with T = 1.
+ *   Supported: K in 1..8, any C >= 1 (16-byte vectors where C and ldx allow
+ *   them), B*T*C < 2^31.  Both states are ignored when K = 1.
+ */
+GDR_API gdr_status gdr_conv_fwd(int B, int T, int C, int K, gdr_dtype dt, int silu, const void *x, int ldx,
+                        const float *w, const float *bias, const void *conv_state_in,
+                        void *conv_state_out, void *y, gdr_stream_t stream);
+
+/*
+ * Backward of gdr_conv_fwd: dz = dy SiLU'(z);
+ *     dx[s,c] = sum_j w[c,j] dz[s+K-1-j, c],  dw[c,j] = sum_{b,t} dz[t,c] x[t-K+1+j, c],  dbias[c] = sum_{b,t} dz[t,c]
+ *   in : the forward's inputs; dy [B,T,C] (dtype dt, dense); dconv_state_out
+ *        [B,K-1,C] (dtype dt) or NULL: the gradient of the returned window,
+ *        which adds to the last K-1 inputs (carried ones where T < K-1).
+ *   out: dx [B,T,C] (dtype dt, dense); dw [C,K] fp32; dbias [C] fp32 or NULL;
+ *        dconv_state_in [B,K-1,C] (dtype dt) or NULL.  All are overwritten;
+ *        the tap sums are joined in a fixed order.
+ *   workspace: gdr_conv_bwd_workspace_bytes(B, T, C, K) bytes.
+ */
+GDR_API gdr_status gdr_conv_bwd(int B, int T, int C, int K, gdr_dtype dt, int silu, const void *x, int ldx,
+                        const float *w, const float *bias, const void *conv_state_in,
+                        const void *dy, const void *dconv_state_out,
+                        void *dx, float *dw, float *dbias, void *dconv_state_in,
+                        void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+GDR_API size_t gdr_conv_bwd_workspace_bytes(int B, int T, int C, int K);
+
+/*
+ * Layer norm over the last axis of R rows, with the residual stream:
+ *     h = x + residual (rounded to dt; h = x without one),
+ *     y = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias      (var: mean of squares)
+ *   in : x, residual [R,D] (dtype dt; residual may be NULL); weight, bias [D]
+ *        fp32 (bias may be NULL); eps >= 0.
+ *   out: y [R,D]; h [R,D] (dtype dt), given exactly when residual is.
+ *   Supported: 1 <= D <= 16384, R < 2^31.
+ */
+GDR_API gdr_status gdr_layernorm_fwd(int64_t R, int D, gdr_dtype dt, const void *x, const void *residual,
+                             const float *weight, const float *bias, float eps, void *y, void *h,
+                             gdr_stream_t stream);
+
+/*
+ * Backward of gdr_layernorm_fwd, from the stored stream h (x without a
+ * residual).  With n = (h - mean)/sqrt(var + eps), g = dy weight:
+ *     dx = (g - mean(g) - n mean(g n)) / sqrt(var + eps) + dres,
+ *     dweight = sum_rows dy n,   dbias = sum_rows dy
+ *   dres [R,D] (dtype dt) or NULL: the gradient that reaches h along the
+ *   residual stream.  dx is the gradient of x and of residual.
+ *   out: dx [R,D] (dtype dt); dweight [D] fp32; dbias [D] fp32 or NULL.
+ *   workspace: gdr_layernorm_bwd_workspace_bytes(D) bytes (partial sums,
+ *   joined in a fixed order).
+ */
+GDR_API gdr_status gdr_layernorm_bwd(int64_t R, int D, gdr_dtype dt, const void *h, const float *weight,
+                             float eps, const void *dy, const void *dres, void *dx, float *dweight,
+                             float *dbias, void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+GDR_API size_t gdr_layernorm_bwd_workspace_bytes(int D);
 
 /* Synchronise `stream`, then read and clear the device status word that
  * kernels set when a bounded wait gives up (GDR_ERR_TIMEOUT).  Returns

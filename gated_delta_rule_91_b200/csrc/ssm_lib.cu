@@ -9,6 +9,7 @@
 #include "layernorm.cuh"
 #include "ssm_simt.cuh"
 #include "ssm_step.cuh"
+#include "ssm_tc.cuh"
 
 namespace gdr {
 
@@ -50,9 +51,19 @@ gdr_status check_stride(const char *fn, const char *name, int *ld, int width, gd
     return GDR_OK;
 }
 
+// bf16 runs on the tensor cores; GDR_SSM_KERNEL=simt selects the CUDA-core
+// kernels (used to cross-check them).  The workspace follows the same choice.
+bool ssm_uses_tc(gdr_dtype dt) {
+    const char *sel = getenv("GDR_SSM_KERNEL");
+    return dt == GDR_BF16 && !(sel != nullptr && strcmp(sel, "simt") == 0);
+}
+
 #define SSM_SHAPES(fn, T, a, ...)                                                  \
     ((a).P == 128 ? ((a).N == 128 ? fn<T, 128, 128>(__VA_ARGS__) : fn<T, 128, 64>(__VA_ARGS__)) \
                   : ((a).N == 128 ? fn<T, 64, 128>(__VA_ARGS__) : fn<T, 64, 64>(__VA_ARGS__)))
+#define SSM_TC_SHAPES(fn, a, ...)                                            \
+    ((a).P == 128 ? ((a).N == 128 ? fn<128, 128>(__VA_ARGS__) : fn<128, 64>(__VA_ARGS__)) \
+                  : ((a).N == 128 ? fn<64, 128>(__VA_ARGS__) : fn<64, 64>(__VA_ARGS__)))
 
 gdr_status check_conv(const char *fn, int B, int T, int C, int K, gdr_dtype dt, int *ldx) {
     if (B < 1 || T < 1 || C < 1)
@@ -84,7 +95,7 @@ extern "C" {
 
 size_t gdr_ssm_fwd_workspace_bytes(int B, int T, int H, int G, int P, int N, gdr_dtype dt) {
     if (check_ssm("gdr_ssm_fwd_workspace_bytes", B, T, H, G, P, N, dt) != GDR_OK) return 0;
-    return ssm_simt_ws(B, T, H, P, N).fwd_total;
+    return ssm_uses_tc(dt) ? ssm_tc_fwd_ws(B, T, H, P, N).total : ssm_simt_ws(B, T, H, P, N).fwd_total;
 }
 
 gdr_status gdr_ssm_fwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, int softplus, const void *x, int ldx,
@@ -117,8 +128,9 @@ gdr_status gdr_ssm_fwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, i
     a.delta = delta; a.A = A; a.D = D; a.bias = delta_bias; a.softplus = softplus; a.S0 = S0;
     a.y = y; a.S_T = S_T;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = dt == GDR_F32 ? SSM_SHAPES(ssm_simt_fwd, float, a, a, workspace, s)
-                                  : SSM_SHAPES(ssm_simt_fwd, __nv_bfloat16, a, a, workspace, s);
+    cudaError_t e = ssm_uses_tc(dt)   ? SSM_TC_SHAPES(ssm_tc_fwd, a, a, workspace, s)
+                    : dt == GDR_F32 ? SSM_SHAPES(ssm_simt_fwd, float, a, a, workspace, s)
+                                    : SSM_SHAPES(ssm_simt_fwd, __nv_bfloat16, a, a, workspace, s);
     if (e != cudaSuccess) return cuda_fail(e, fn);
     return GDR_OK;
 }

@@ -268,7 +268,7 @@ __device__ __forceinline__ void ssm_tc_tables(const float *s_dt, const double *s
 }
 
 template <int P, int N, bool LO>
-__global__ void __launch_bounds__(256) ssm_tc_y_kernel(const __grid_constant__ CUtensorMap tm_x,
+__global__ void __launch_bounds__(256, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(const __grid_constant__ CUtensorMap tm_x,
                                                        const __grid_constant__ CUtensorMap tm_b,
                                                        const __grid_constant__ CUtensorMap tm_c,
                                                        const __grid_constant__ CUtensorMap tm_y, SsmArgs a, int m,

@@ -243,11 +243,13 @@ def test_graph_replay_and_other_stream():
         assert torch.equal(y0, y2) and torch.equal(S0, S2) and all(torch.equal(g0[k], g2[k]) for k in g0)
 
 
-def test_workspace_of_exact_size_is_not_overrun():
-    d = inputs(1, 200, 2, 1, 64, 64, "bf16", seed=13)
-    L = gdr.lib()
-    for need, call in ((L.gdr_ssm_fwd_workspace_bytes(1, 200, 2, 1, 64, 64, gdr.GDR_BF16), fwd),
-                       (L.gdr_ssm_bwd_workspace_bytes(1, 200, 2, 1, 64, 64, gdr.GDR_BF16), bwd)):
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_workspace_of_exact_size_is_not_overrun(dtype):
+    d = inputs(1, 1500, 2, 1, 64, 64, dtype, seed=13)
+    L, dt = gdr.lib(), gdr.GDR_F32 if dtype == "f32" else gdr.GDR_BF16
+    for need, call in ((L.gdr_ssm_fwd_workspace_bytes(1, 1500, 2, 1, 64, 64, dt), fwd),
+                       (L.gdr_ssm_bwd_workspace_bytes(1, 1500, 2, 1, 64, 64, dt), bwd)):
+        assert need > 0
         buf = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
         call(d, workspace=buf[:need])
         assert (buf[need:] == 77).all()

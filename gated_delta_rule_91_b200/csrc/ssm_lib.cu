@@ -10,6 +10,7 @@
 #include "ssm_simt.cuh"
 #include "ssm_step.cuh"
 #include "ssm_tc.cuh"
+#include "ssm_bwd_tc.cuh"
 
 namespace gdr {
 
@@ -137,7 +138,7 @@ gdr_status gdr_ssm_fwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, i
 
 size_t gdr_ssm_bwd_workspace_bytes(int B, int T, int H, int G, int P, int N, gdr_dtype dt) {
     if (check_ssm("gdr_ssm_bwd_workspace_bytes", B, T, H, G, P, N, dt) != GDR_OK) return 0;
-    return ssm_simt_ws(B, T, H, P, N).bwd_total;
+    return ssm_uses_tc(dt) ? ssm_tc_bwd_ws(B, T, H, G, P, N).total : ssm_simt_ws(B, T, H, P, N).bwd_total;
 }
 
 gdr_status gdr_ssm_bwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, int softplus, const void *x, int ldx,
@@ -180,8 +181,9 @@ gdr_status gdr_ssm_bwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, i
     a.dy = dy; a.dS_T = dS_T;
     a.dx = dx; a.dB = dB; a.dC = dC; a.ddelta = ddelta; a.dA = dA; a.dD = dD; a.dbias = ddelta_bias; a.dS0 = dS0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = dt == GDR_F32 ? SSM_SHAPES(ssm_simt_bwd, float, a, a, workspace, s)
-                                  : SSM_SHAPES(ssm_simt_bwd, __nv_bfloat16, a, a, workspace, s);
+    cudaError_t e = ssm_uses_tc(dt)   ? SSM_TC_SHAPES(ssm_tc_bwd, a, a, workspace, s)
+                    : dt == GDR_F32 ? SSM_SHAPES(ssm_simt_bwd, float, a, a, workspace, s)
+                                    : SSM_SHAPES(ssm_simt_bwd, __nv_bfloat16, a, a, workspace, s);
     if (e != cudaSuccess) return cuda_fail(e, fn);
     return GDR_OK;
 }

@@ -427,29 +427,20 @@ def _rows(name, t, shape, lead, dtype, device):
     return t.data_ptr(), ld or width
 
 
-class _on:
-    """Makes the tensors' device current around a call (launches go to the current device)."""
-
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _launch(device, fn, *args):
+    """fn(*args, stream) on the device's current stream, with the device made current (launches go to that one)."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+    else:
+        with torch.cuda.device(index):
+            check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
 def _cuda(x, name):
     if not x.is_cuda:
         raise ValueError("%s must be on a CUDA device" % name)
     return x.device
-
-
-def _out(name, t, shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else t
 
 
 def _scratch(nbytes, device, workspace):
@@ -486,16 +477,15 @@ def gdr_ssm_fwd(x, delta, A, Bm, Cm, D=None, delta_bias=None, S0=None, *, softpl
     group); all three may be slices of one [B,T,channels] buffer.  delta [B,T,H], A, D, delta_bias [H] fp32; S0
     [B,H,P,N] fp32.  Returns (y, S_T or None)."""
     (B, T), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 2)
-    y = _out("y", y, (B, T, H, P), x.dtype, dev)
+    y = x.new_empty((B, T, H, P)) if y is None else y
     if S_T is None and return_state:
         S_T = torch.empty(B, H, P, N, dtype=torch.float32, device=dev)
     f = torch.float32
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_ssm_fwd_workspace_bytes(B, T, H, G, P, N, dt), dev, workspace)
-    with _on(dev):
-        check(L.gdr_ssm_fwd(B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev),
-                            _like("y", y, (B, T, H, P), x.dtype, dev), _like("S_T", S_T, (B, H, P, N), f, dev),
-                            ws.data_ptr(), ws_bytes, torch.cuda.current_stream(dev).cuda_stream))
+    _launch(dev, L.gdr_ssm_fwd, B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev),
+            _like("y", y, (B, T, H, P), x.dtype, dev), _like("S_T", S_T, (B, H, P, N), f, dev),
+            ws.data_ptr(), ws_bytes)
     return y, S_T
 
 
@@ -511,11 +501,9 @@ def gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, dy, dS_T=None, *, softpl
                ddelta_bias=None if delta_bias is None else e(H), dS0=e(B, H, P, N) if want_dS0 else None)
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_ssm_bwd_workspace_bytes(B, T, H, G, P, N, dt), dev, workspace)
-    with _on(dev):
-        check(L.gdr_ssm_bwd(B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev),
-                            _like("dy", dy, (B, T, H, P), x.dtype, dev), _like("dS_T", dS_T, (B, H, P, N), f, dev),
-                            *(None if t is None else t.data_ptr() for t in out.values()), ws.data_ptr(), ws_bytes,
-                            torch.cuda.current_stream(dev).cuda_stream))
+    _launch(dev, L.gdr_ssm_bwd, B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev),
+            _like("dy", dy, (B, T, H, P), x.dtype, dev), _like("dS_T", dS_T, (B, H, P, N), f, dev),
+            *(None if t is None else t.data_ptr() for t in out.values()), ws.data_ptr(), ws_bytes)
     return out
 
 
@@ -523,14 +511,12 @@ def gdr_ssm_step(x, delta, A, Bm, Cm, S, D=None, delta_bias=None, *, softplus=Fa
     """One token of gdr_ssm_fwd: x [B,H,P]; Bm, Cm [B,G,N]; delta [B,H]; S [B,H,P,N] fp32 advanced in place.
     Returns y [B,H,P]."""
     (B,), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 1)
-    y = _out("y", y, (B, H, P), x.dtype, dev)
+    y = x.new_empty((B, H, P)) if y is None else y
     if S is None:
         raise ValueError("S is required")
-    with _on(dev):
-        check(lib().gdr_ssm_step(B, H, G, P, N, dt, int(softplus), *ptrs,
-                                 _like("S", S, (B, H, P, N), torch.float32, dev),
-                                 _like("y", y, (B, H, P), x.dtype, dev),
-                                 torch.cuda.current_stream(dev).cuda_stream))
+    _launch(dev, lib().gdr_ssm_step, B, H, G, P, N, dt, int(softplus), *ptrs,
+            _like("S", S, (B, H, P, N), torch.float32, dev),
+            _like("y", y, (B, H, P), x.dtype, dev))
     return y
 
 
@@ -551,11 +537,10 @@ def gdr_conv_fwd(x, w, bias=None, *, conv_state=None, conv_state_out=None, silu=
     [C,K] and bias [C] fp32.  conv_state [B,K-1,C] (dtype of x) carries the inputs before token 0; conv_state_out
     receives the last K-1 inputs and may be conv_state itself.  A decode token is T = 1.  Returns y [B,T,C]."""
     B, T, C, K, dt, dev, ptrs = _conv_operands(x, w, bias, conv_state)
-    y = _out("y", y, (B, T, C), x.dtype, dev)
-    with _on(dev):
-        check(lib().gdr_conv_fwd(B, T, C, K, dt, int(silu), *ptrs,
-                                 _like("conv_state_out", conv_state_out, (B, max(K - 1, 0), C), x.dtype, dev),
-                                 _like("y", y, (B, T, C), x.dtype, dev), torch.cuda.current_stream(dev).cuda_stream))
+    y = x.new_empty((B, T, C)) if y is None else y
+    _launch(dev, lib().gdr_conv_fwd, B, T, C, K, dt, int(silu), *ptrs,
+            _like("conv_state_out", conv_state_out, (B, max(K - 1, 0), C), x.dtype, dev),
+            _like("y", y, (B, T, C), x.dtype, dev))
     return y
 
 
@@ -572,11 +557,9 @@ def gdr_conv_bwd(x, w, dy, bias=None, *, conv_state=None, dconv_state_out=None, 
                dconv_state=torch.empty(B, max(K - 1, 0), C, dtype=x.dtype, device=dev) if want_ds else None)
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_conv_bwd_workspace_bytes(B, T, C, K), dev, workspace)
-    with _on(dev):
-        check(L.gdr_conv_bwd(B, T, C, K, dt, int(silu), *ptrs, _like("dy", dy, (B, T, C), x.dtype, dev),
-                             _like("dconv_state_out", dconv_state_out, (B, max(K - 1, 0), C), x.dtype, dev),
-                             *(None if t is None else t.data_ptr() for t in out.values()), ws.data_ptr(), ws_bytes,
-                             torch.cuda.current_stream(dev).cuda_stream))
+    _launch(dev, L.gdr_conv_bwd, B, T, C, K, dt, int(silu), *ptrs, _like("dy", dy, (B, T, C), x.dtype, dev),
+            _like("dconv_state_out", dconv_state_out, (B, max(K - 1, 0), C), x.dtype, dev),
+            *(None if t is None else t.data_ptr() for t in out.values()), ws.data_ptr(), ws_bytes)
     return out
 
 
@@ -584,17 +567,15 @@ def gdr_layernorm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, 
     """Layer norm of h = x + residual over the last axis (x [...,D]; weight, bias [D] fp32).  Returns (y, h); h is
     None without a residual."""
     dev, dt, D = _cuda(x, "x"), _dt(x), x.shape[-1]
-    y = _out("y", y, x.shape, x.dtype, dev)
+    y = x.new_empty(x.shape) if y is None else y
     if residual is not None and h is None:
         h = torch.empty(x.shape, dtype=x.dtype, device=dev)
     f = torch.float32
-    with _on(dev):
-        check(lib().gdr_layernorm_fwd(x.numel() // max(D, 1), D, dt, _like("x", x, x.shape, x.dtype, dev),
-                                      _like("residual", residual, x.shape, x.dtype, dev),
-                                      _like("weight", weight, (D,), f, dev), _like("bias", bias, (D,), f, dev),
-                                      float(eps), _like("y", y, x.shape, x.dtype, dev),
-                                      _like("h", h, x.shape, x.dtype, dev),
-                                      torch.cuda.current_stream(dev).cuda_stream))
+    _launch(dev, lib().gdr_layernorm_fwd, x.numel() // max(D, 1), D, dt, _like("x", x, x.shape, x.dtype, dev),
+            _like("residual", residual, x.shape, x.dtype, dev),
+            _like("weight", weight, (D,), f, dev), _like("bias", bias, (D,), f, dev),
+            float(eps), _like("y", y, x.shape, x.dtype, dev),
+            _like("h", h, x.shape, x.dtype, dev))
     return y, h
 
 
@@ -608,10 +589,9 @@ def gdr_layernorm_bwd(h, weight, dy, *, dres=None, eps=1e-5, want_dbias=True, wo
     dbias = torch.empty(D, dtype=f, device=dev) if want_dbias else None
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_layernorm_bwd_workspace_bytes(D), dev, workspace)
-    with _on(dev):
-        check(L.gdr_layernorm_bwd(h.numel() // max(D, 1), D, dt, _like("h", h, h.shape, h.dtype, dev),
-                                  _like("weight", weight, (D,), f, dev), float(eps),
-                                  _like("dy", dy, h.shape, h.dtype, dev), _like("dres", dres, h.shape, h.dtype, dev),
-                                  dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
-                                  ws.data_ptr(), ws_bytes, torch.cuda.current_stream(dev).cuda_stream))
+    _launch(dev, L.gdr_layernorm_bwd, h.numel() // max(D, 1), D, dt, _like("h", h, h.shape, h.dtype, dev),
+            _like("weight", weight, (D,), f, dev), float(eps),
+            _like("dy", dy, h.shape, h.dtype, dev), _like("dres", dres, h.shape, h.dtype, dev),
+            dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
+            ws.data_ptr(), ws_bytes)
     return dx, dweight, dbias

@@ -75,48 +75,6 @@ template <int CPL> __device__ __forceinline__ void st_row(__nv_bfloat16 *p, cons
     }
 }
 
-// Special-function-unit approximations with denormals flushed (ex2.approx,
-// rcp.approx, rsqrt.approx of the PTX ISA).
-__device__ __forceinline__ float ex2_ftz(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp_ftz(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rsqrt_ftz(float x) {
-    float y;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// SiLU(z) = z / (1 + e^-z), with e^-z = 2^(-z log2 e).  For z -> -inf the
-// denominator overflows to +inf, its reciprocal is 0 and the result -0, the
-// limit; for z -> +inf the result is z.
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float silu_f(float z) { return z * rcp_ftz(1.f + ex2_ftz(-kLog2e * z)); }
-
-// Packed fp32 pair arithmetic (fma.rn.f32x2 / mul.rn.f32x2): one instruction
-// for two lanes' worth of FMAs, each rounded as the scalar one.
-__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n .reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n"
-        " mov.b64 rc, {%6, %7};\n fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0, %1}, rd;\n}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n"
-        " mul.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // ---- prologue -------------------------------------------------------------------
 struct PrologueArgs {
     int B, T, H, dk, dv, K;

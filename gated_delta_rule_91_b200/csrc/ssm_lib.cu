@@ -78,8 +78,11 @@ gdr_status check_conv(const char *fn, int B, int T, int C, int K, gdr_dtype dt, 
     return GDR_OK;
 }
 
-// Vectors need every row of every tensor to start on a vector boundary.
-bool conv_vectors(const ConvArgs &a, int v) { return a.C % v == 0 && a.ldx % v == 0; }
+// The vector form copies 16 bytes at a time: every row of every tensor has to start on 16 bytes.
+bool conv_vectors(const ConvArgs &a, gdr_dtype dt) {
+    const int v = dt == GDR_F32 ? 4 : 8;
+    return a.C % v == 0 && a.ldx % v == 0;
+}
 
 gdr_status check_norm(const char *fn, long long R, int D, gdr_dtype dt, float eps) {
     if (R < 1 || D < 1) return fail(GDR_ERR_INVALID_ARGUMENT, "%s: sizes must be positive (rows=%lld D=%d)", fn, R, D);
@@ -239,9 +242,9 @@ gdr_status gdr_conv_fwd(int B, int T, int C, int K, gdr_dtype dt, int silu, cons
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (dt == GDR_F32)
-        e = conv_vectors(a, 4) ? conv_fwd_width<float, 4>(K, a, s) : conv_fwd_width<float, 1>(K, a, s);
+        e = conv_vectors(a, dt) ? conv_fwd_width<float, 4>(K, a, s) : conv_fwd_width<float, 1>(K, a, s);
     else
-        e = conv_vectors(a, 8) ? conv_fwd_width<__nv_bfloat16, 8>(K, a, s) : conv_fwd_width<__nv_bfloat16, 1>(K, a, s);
+        e = conv_vectors(a, dt) ? conv_fwd_width<__nv_bfloat16, 4>(K, a, s) : conv_fwd_width<__nv_bfloat16, 1>(K, a, s);
     if (e != cudaSuccess) return cuda_fail(e, fn);
     return GDR_OK;
 }
@@ -285,9 +288,9 @@ gdr_status gdr_conv_bwd(int B, int T, int C, int K, gdr_dtype dt, int silu, cons
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (dt == GDR_F32)
-        e = conv_vectors(a, 4) ? conv_bwd_width<float, 4>(K, a, dw, dbias, s) : conv_bwd_width<float, 1>(K, a, dw, dbias, s);
+        e = conv_vectors(a, dt) ? conv_bwd_width<float, 4>(K, a, dw, dbias, s) : conv_bwd_width<float, 1>(K, a, dw, dbias, s);
     else
-        e = conv_vectors(a, 4) ? conv_bwd_width<__nv_bfloat16, 4>(K, a, dw, dbias, s)
+        e = conv_vectors(a, dt) ? conv_bwd_width<__nv_bfloat16, 4>(K, a, dw, dbias, s)
                                : conv_bwd_width<__nv_bfloat16, 1>(K, a, dw, dbias, s);
     if (e != cudaSuccess) return cuda_fail(e, fn);
     return GDR_OK;

@@ -35,7 +35,6 @@ namespace gdr {
 
 constexpr int kTcQ = 128;
 constexpr uint32_t kTile = 128 * 128;  // 128 rows x 64 bf16, 128B swizzle
-constexpr float kLog2e = 1.4426950408889634f;
 
 // ---- tensor maps ----------------------------------------------------------------------
 typedef CUresult (*SsmEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,

@@ -1,10 +1,10 @@
 // ssm_bwd_tc.cuh -- the selective scan's gradients on the 5th-generation
 // tensor cores, bf16 inputs, P, N in {64, 128}; formulas at the gradient kernel
 // of ssm_simt.cuh.  Chunks of 128 tokens:
-//   1. ssm_tc_state_kernel per chunk: U_c and V_c, every weighted row in two
-//      bf16 parts
-//   2. ssm_scan_kernel over the chunks, fp32: S_in(c), and in reverse G_out(c)
-//   3. ssm_tc_grad_kernel: a CTA owns one chunk of one group and walks heads of
+//   1. ssm_tc_walk_kernel   S_in(c) of every chunk, walking forwards, and G_out(c),
+//      walking backwards, in one launch (segments from ssm_tc_state_kernel and
+//      ssm_scan_kernel first where heads are few), each state as two bf16 parts
+//   2. ssm_tc_grad_kernel   a CTA owns one chunk of one group and walks heads of
 //      it, so that C B^T is formed once and dB, dC are summed over the heads in
 //      TMEM.  Per head (W = dy x^T, L the decays, tokens on the TMEM lanes):
 //        W   = dY X^T                              N = 128   K = P
@@ -23,18 +23,187 @@
 
 namespace gdr {
 
+// A state's two bf16 parts in memory: [unit][part][N][P], unit = (b, chunk, head).
+inline bool ssm_state_map(CUtensorMap *map, const void *base, size_t units, int P, int N) {
+    SsmEncodeFn enc = ssm_encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)P, (cuuint64_t)N, 2, (cuuint64_t)units};
+    const cuuint64_t strides[3] = {(cuuint64_t)P * 2, (cuuint64_t)N * P * 2, (cuuint64_t)2 * N * P * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)N, 1, 1}, estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---- 1. the states of every chunk --------------------------------------------------------
+// A CTA walks the chunks of one (b, h, segment) for 64 columns p of the state, forwards (S) or backwards (G); the
+// state stays in TMEM (lanes n, fp32).  Per chunk: write the state as it enters (in walking order), scale it by the
+// chunk's decay, and add (w B)^T X, or (e^c C)^T dY, with the weighted rows in two bf16 parts (the first in place).
+template <int N>
+struct SsmWalkTc {
+    static constexpr uint32_t BB = N / 64 * kTile;
+    static constexpr uint32_t oX = 0, oHi = kTile, oLo = oHi + BB, oZero = oLo + BB;
+    static constexpr uint32_t kHiBlock = N == 64 ? 2 * kTile : kTile;
+    static constexpr uint32_t oCtl = oZero + (N == 64 ? kTile : 0);
+    static constexpr uint32_t kAlloc = oCtl + 2 * 128 * 12 + 128 + 1024;
+};
+
+template <int P, int N>
+__global__ void __launch_bounds__(256, 2) ssm_tc_walk_kernel(
+    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
+    const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_c, SsmArgs a, int m,
+    const float *__restrict__ seg_S, const float *__restrict__ seg_G, __nv_bfloat16 *__restrict__ out_S,
+    __nv_bfloat16 *__restrict__ out_G) {
+    using L = SsmWalkTc<N>;
+    using namespace sm100;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const uint32_t sb = smem_u32(sm);
+    double *s_c2 = reinterpret_cast<double *>(sm + L::oCtl);
+    float *s_dt2 = reinterpret_cast<float *>(s_c2 + 256);
+    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(s_dt2 + 256), *mma_bar = tma_bar + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tma_bar + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+    const int nch = (a.T + kTcQ - 1) / kTcQ, R = (nch + m - 1) / m;
+    int u = blockIdx.x;
+    const bool rev = u & 1;
+    u >>= 1;
+    const int p0 = P == 128 ? (u & 1) * 64 : 0;
+    if (P == 128) u >>= 1;
+    const int seg = u % R, bh = u / R, h = bh % a.H, b = bh / a.H, g = h / (a.H / a.G);
+    const int c0 = seg * m, cn = min(m, nch - c0);
+    auto chunk = [&](int k) { return rev ? c0 + cn - 1 - k : c0 + k; };
+
+    if (tid == 0) {
+        mbar_init(tma_bar, 1);
+        mbar_init(mma_bar, 1);
+        fence_mbar_init();
+        *abort_flag = 0;
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, 64);
+    if (N == 64)
+        for (int i = tid; i < (int)kTile / 16; i += 256) reinterpret_cast<uint4 *>(sm + L::oZero)[i] = make_uint4(0, 0, 0, 0);
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + half * 32;
+    auto issue = [&](int k) {
+        mbar_expect_tx(tma_bar, kTile + L::BB);
+        tma_load_4d(sm + L::oX, rev ? &tm_dy : &tm_x, tma_bar, p0, h, chunk(k) * kTcQ, b);
+        for (int i = 0; i < N / 64; ++i)
+            tma_load_4d(sm + L::oHi + i * kTile, rev ? &tm_c : &tm_b, tma_bar, i * 64, g, chunk(k) * kTcQ, b);
+    };
+    if (tid == 0) issue(0);
+    if (warp == 1) ssm_tc_gates(a, b, h, chunk(0) * kTcQ, s_dt2, s_c2);
+    float v[32];
+    {
+        const float *src = R > 1 ? (rev ? seg_G : seg_S) + (((size_t)b * R + seg) * a.H + h) * P * N
+                                 : (rev ? a.dS_T : a.S0);
+        if (R == 1 && src) src += (size_t)bh * P * N;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = src && row < N ? src[(size_t)(p0 + half * 32 + i) * N + row] : 0.f;
+        tmem_st32(tl, v);
+        tmem_wait_st();
+    }
+    __syncthreads();
+    bool pending = false;
+    int k = 0;
+#pragma unroll 1
+    for (; k < cn; ++k) {
+        const double *s_c = s_c2 + (k & 1) * 128;
+        const float *s_dt = s_dt2 + (k & 1) * 128;
+        const double last = s_c[127];
+        if (row < N) {  // the state as it enters, and its decay
+            const float el = exp2f((float)last);
+            const size_t unit = ((size_t)b * nch + chunk(k)) * a.H + h;
+            uint8_t *hi = reinterpret_cast<uint8_t *>((rev ? out_G : out_S) + ((unit * 2) * N + row) * P + p0 + half * 32);
+            uint8_t *lo = hi + (size_t)N * P * 2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_split8(hi + 16 * i, lo + 16 * i, v + 8 * i);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= el;
+            tmem_st32(tl, v);
+            tmem_wait_st();
+        }
+        const bool last_one = k + 1 == cn && !(rev && seg == 0 && a.dS0);  // nothing reads the state after it
+        if (tid == 0 && !mbar_wait(tma_bar, (uint32_t)(k & 1))) *abort_flag = 1;
+        __syncthreads();
+        if (*abort_flag || last_one) break;
+        {
+            const int r = tid & 127, hf = tid >> 7;
+            const float w = rev ? exp2f((float)s_c[r]) : s_dt[r] * exp2f((float)(last - s_c[r]));
+            constexpr int CH = N / 16;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int c = hf * CH + i;
+                const uint32_t off = (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
+                float x[8];
+                ld8s(sm + L::oHi + off, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= w;
+                st_split8(sm + L::oHi + off, sm + L::oLo + off, x);
+            }
+        }
+        fence_async_smem();
+        tc_before_sync();
+        __syncthreads();
+        if (tid == 0) {
+            tc_after_sync();
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16(tmem, desc_mn(sb + (part ? L::oLo : L::oHi), kk, part ? kTile : L::kHiBlock),
+                             desc_mn(sb + L::oX, kk), idesc_bf16(128, 64, true, true), 1);
+            mma_commit(mma_bar);
+        }
+        if (warp == 1 && k + 1 < cn)
+            ssm_tc_gates(a, b, h, chunk(k + 1) * kTcQ, s_dt2 + ((k + 1) & 1) * 128, s_c2 + ((k + 1) & 1) * 128);
+        if (tid == 0) {
+            if (!mbar_wait(mma_bar, (uint32_t)(k & 1))) {
+                *abort_flag = 1;
+                pending = true;
+            } else if (k + 1 < cn) {
+                issue(k + 1);
+            }
+        }
+        __syncthreads();
+        if (*abort_flag) break;
+        tc_after_sync();
+        tmem_ld32(tl, v);
+    }
+    if (*abort_flag) {
+        if (tid == 0) {
+            record_status(GDR_ERR_TIMEOUT);
+            mbar_wait(pending ? mma_bar : tma_bar, (uint32_t)(k & 1));
+        }
+    } else if (rev && seg == 0 && a.dS0 && row < N) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a.dS0[((size_t)bh * P + p0 + half * 32 + i) * N + row] = v[i];
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tc_after_sync();
+        tmem_dealloc(tmem, 64);
+    }
+}
+
+// ---- 2. the gradients of every chunk -------------------------------------------------------
 template <int P, int N>
 struct SsmGradTc {
     static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile;
-    static constexpr uint32_t kSBlock = P * 128, SB = N / 64 * kSBlock;  // a state part: P rows, blocks of 64 columns n
+    static constexpr uint32_t kSBlock = N * 128, SB = P / 64 * kSBlock;  // a state part: N rows, blocks of 64 columns p
     static constexpr uint32_t oB = 0, oC = BB, oX = 2 * BB, oY = oX + XB, oR = oY + XB;
     static constexpr uint32_t oM = oR, oK = oR + 2 * kTile;   // M', dK
     static constexpr uint32_t oHi = oR, oLo = oR + SB;        // S_in, then G_out
     static constexpr uint32_t oGate = oR + 4 * kTile;
-    // doubles c[2][128], red[2][8]; floats dt[2][128], e, row, el, hi, lo [128], col[288]; per head, two sets:
-    // rowp[2][128], colp[4][128], diag, wd, gxp[2][128], syp[2][128] and four joined arrays of 128
-    static constexpr uint32_t kSet = (2 + 4 + 1 + 1 + 2 + 2) * 128;
-    static constexpr uint32_t kGate = (256 + 16) * 8 + (256 + 5 * 128 + 288 + 2 * kSet + 4 * 128) * 4;
+    // doubles: warp sums of c [4], of the token sums [4][2], totals [4][3], <G, S> [16]; floats dt, e, row, el, hi, lo
+    // [128], col[288], rowp[4][128], colp[4][128], diag, wd, gxp[4][128], syp[4][128]
+    static constexpr uint32_t kGate = (4 + 8 + 12 + 16) * 8 + (6 * 128 + 288 + 18 * 128) * 4;
     static constexpr uint32_t oBar = oGate + kGate;
     static constexpr uint32_t kAlloc = oBar + 64 + 1024;
 };
@@ -52,31 +221,47 @@ __device__ __forceinline__ void ssm_column_sums(float *v) {
         }
     }
 }
+__device__ __forceinline__ double ssm_warp_scan(double x) {  // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += o;
+    }
+    return x;
+}
+__device__ __forceinline__ double ssm_warp_sum(double x) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
 
-constexpr int kGradThreads = 288;  // 8 warps of tokens, and one for the gates and the per-token sums
+constexpr int kGradThreads = 512;  // a TMEM quarter and a quarter of the columns per warp
 
 template <int P, int N>
 __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_dy,
-    const __grid_constant__ CUtensorMap tm_dx, SsmArgs a, int splits, int per, const float *__restrict__ Sin,
-    const float *__restrict__ Gout, float *__restrict__ dBp, float *__restrict__ dCp, float *__restrict__ part) {
+    const __grid_constant__ CUtensorMap tm_dx, const __grid_constant__ CUtensorMap tm_s,
+    const __grid_constant__ CUtensorMap tm_g, SsmArgs a, int splits, int per, const __nv_bfloat16 *__restrict__ Sin,
+    const __nv_bfloat16 *__restrict__ Gout, float *__restrict__ dBp, float *__restrict__ dCp, float *__restrict__ part) {
     using L = SsmGradTc<P, N>;
     using namespace sm100;
+    constexpr int NW = N / 4, PW = P / 4;  // columns of a warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
-    double *s_c2 = reinterpret_cast<double *>(sm + L::oGate), *s_red2 = s_c2 + 256;
-    float *s_dt2 = reinterpret_cast<float *>(s_red2 + 16);
-    float *s_e = s_dt2 + 256, *s_rowf = s_e + 128, *s_el = s_rowf + 128, *s_hi = s_el + 128, *s_lo = s_hi + 128;
-    float *s_col = s_lo + 128, *s_set = s_col + 288, *s_join = s_set + 2 * L::kSet;
+    double *s_cw = reinterpret_cast<double *>(sm + L::oGate), *s_tw = s_cw + 4, *s_tot = s_tw + 8, *s_red = s_tot + 12;
+    float *s_dt = reinterpret_cast<float *>(s_red + 16);
+    float *s_e = s_dt + 128, *s_rowf = s_e + 128, *s_el = s_rowf + 128, *s_hi = s_el + 128, *s_lo = s_hi + 128;
+    float *s_col = s_lo + 128, *s_rowp = s_col + 288, *s_colp = s_rowp + 512, *s_diag = s_colp + 512, *s_wd = s_diag + 128,
+          *s_gxp = s_wd + 128, *s_syp = s_gxp + 512;
     uint64_t *bar_bc = reinterpret_cast<uint64_t *>(sm + L::oBar), *bar_x = bar_bc + 1, *bar_y = bar_bc + 2,
-             *mma_bar = bar_bc + 3;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_bc + 4);
+             *bar_s = bar_bc + 3, *mma_bar = bar_bc + 4;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_bc + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int q = warp & 3, half = (warp >> 2) & 1, row = q * 32 + lane;
-    const bool worker = warp < 8;  // one lane of a TMEM quarter and half of the columns each
+    const int q = warp & 3, prt = warp >> 2, row = q * 32 + lane;  // TMEM lane, column quarter
     const int nch = (a.T + kTcQ - 1) / kTcQ, HG = a.H / a.G;
     int u = blockIdx.x;
     const int sp = u % splits;
@@ -86,11 +271,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     const int ch = u % nch, b = u / nch;
     const int h0 = g * HG + sp * per, nh = min(per, HG - sp * per);
     const int t0 = ch * kTcQ, valid = min(kTcQ, a.T - t0);
+    const size_t unit0 = ((size_t)b * nch + ch) * a.H, units = (size_t)a.B * nch * a.H;
 
     if (tid == 0) {
         mbar_init(bar_bc, 1);
         mbar_init(bar_x, 1);
         mbar_init(bar_y, 1);
+        mbar_init(bar_s, 1);
         mbar_init(mma_bar, 1);
         fence_mbar_init();
         *abort_flag = 0;
@@ -103,7 +290,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     constexpr uint32_t tK = 0, tT = 128, tC = 256, tB = 256 + N;
 
-    int n_x = 0, n_y = 0, d_x = 0, d_y = 0;
+    int n_x = 0, n_y = 0, n_s = 0, d_x = 0, d_y = 0;  // thread 0's
+    uint32_t s_phase = 0;                             // everyone's
     bool bc_open = false, mma_open = false;
     auto issue_x = [&](int h) {
         mbar_expect_tx(bar_x, L::XB);
@@ -115,6 +303,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         for (int i = 0; i < P / 64; ++i) tma_load_4d(sm + L::oY + i * kTile, &tm_dy, bar_y, i * 64, h, t0, b);
         ++n_y;
     };
+    auto issue_state = [&](const CUtensorMap *map, size_t unit) {
+        mbar_expect_tx(bar_s, 2 * L::SB);
+        for (int pt = 0; pt < 2; ++pt)
+            for (int i = 0; i < P / 64; ++i)
+                tma_load_4d(sm + L::oHi + pt * L::SB + i * L::kSBlock, map, bar_s, i * 64, 0, pt, (int)unit);
+        ++n_s;
+    };
+    auto wait_state = [&] {  // every thread
+        if (!mbar_wait(bar_s, s_phase)) *abort_flag = 1;
+        s_phase ^= 1;
+    };
     if (tid == 0) {
         mbar_expect_tx(bar_bc, 2 * L::BB);
         for (int i = 0; i < N / 64; ++i) {
@@ -125,10 +324,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         issue_x(h0);
         issue_y(h0);
     }
-    if (warp == 8) ssm_tc_gates(a, b, h0, t0, s_dt2, s_c2);
-    __syncthreads();
-
-    auto worker_sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     uint32_t mma_phase = 0;
     auto mma_sync_point = [&]() {
         if (tid == 0) {
@@ -137,78 +332,56 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             if (mma_open) *abort_flag = 1;
         }
         mma_phase ^= 1;
-        worker_sync();
+        __syncthreads();
         tc_after_sync();
     };
-    const size_t units = (size_t)a.B * nch * a.H;
-    // 8 columns of row p = 0 .. P-1 of a state: chunk i of this thread
-    constexpr int kChunks = P * N / 8 / 256;
-    auto chunk_p = [&](int i) { return (i * 256 + tid) / (N / 8); };
-    auto chunk_n = [&](int i) { return (i * 256 + tid) % (N / 8); };
+    // 8 columns p of a row n of a state: chunk i of this thread
+    constexpr int kChunks = P * N / 8 / kGradThreads;
     auto chunk_off = [&](int i) {
-        const int p = chunk_p(i), n8 = chunk_n(i);
-        return (uint32_t)(n8 >> 3) * L::kSBlock + sw128_offset(p, n8 & 7);
+        const int n = (i * kGradThreads + tid) / (P / 8), p8 = (i * kGradThreads + tid) % (P / 8);
+        return (uint32_t)(p8 >> 3) * L::kSBlock + sw128_offset(n, p8 & 7);
     };
-    auto load_state = [&](const float *src, float (&v)[kChunks][8]) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) load8(src + (size_t)(i * 256 + tid) * 8, v[i]);
+    auto raw_delta = [&](int h) {
+        float z = t0 + tid < a.T ? a.delta[((size_t)b * a.T + t0 + tid) * a.H + h] : 0.f;
+        if (a.bias) z += a.bias[h];
+        return z;
     };
+    float z_next = tid < 128 ? raw_delta(h0) : 0.f;
 
-    // Warps 0-7 walk the heads (barrier 1 among themselves); warp 8 prepares the next head's gates and finishes the
-    // last head's per-token sums beside them.  All meet once a head, at barrier 0.
-    auto token_sums = [&](int hh) {
-        const int set = hh & 1;
-        const float *s_rowp = s_set + set * L::kSet, *s_colp = s_rowp + 256, *s_diag = s_colp + 512, *s_wd = s_diag + 128,
-                    *s_gxp = s_wd + 128, *s_syp = s_gxp + 256;
-        for (int t = lane; t < 128; t += 32) {
-            s_join[t] = s_colp[t] + s_colp[128 + t] + s_colp[256 + t] + s_colp[384 + t];
-            s_join[128 + t] = s_rowp[t] + s_rowp[128 + t];
-            s_join[256 + t] = s_gxp[t] + s_gxp[128 + t];
-            s_join[384 + t] = s_syp[t] + s_syp[128 + t];
-        }
-        __syncwarp();
-        double cross = 0.0;
-        for (int w = 0; w < 8; ++w) cross += s_red2[set * 8 + w];
-        ssm_token_grads(a, b, h0 + hh, t0, valid, kTcQ, s_dt2 + set * 128, s_join, s_diag, s_join + 128, s_join + 256,
-                        s_join + 384, cross * exp2(s_c2[set * 128 + 127]), s_wd, part,
-                        ((size_t)b * nch + ch) * a.H + h0 + hh, units);
-        __syncwarp();
-    };
-    if (!worker) {
 #pragma unroll 1
-        for (int hh = 0; hh <= nh; ++hh) {
-            __syncthreads();
-            if (*abort_flag) break;
-            if (hh > 0) token_sums(hh - 1);
-            if (hh + 1 < nh) ssm_tc_gates(a, b, h0 + hh + 1, t0, s_dt2 + ((hh + 1) & 1) * 128, s_c2 + ((hh + 1) & 1) * 128);
+    for (int hh = 0; hh < nh; ++hh) {
+        const int h = h0 + hh;
+        const size_t unit = unit0 + h;
+        const float z = z_next;
+        if (tid < 2 * P * N * 2 / 128) {  // this head's states on their way into L2: a line of each a thread
+            prefetch_l2(reinterpret_cast<const uint8_t *>(Sin) + unit * 4 * P * N + tid * 128);
+            prefetch_l2(reinterpret_cast<const uint8_t *>(Gout) + unit * 4 * P * N + tid * 128);
         }
-    }
-    int hh = 0;
-#pragma unroll 1
-    for (; worker && hh < nh; ++hh) {
+        // ---- gates: token tid ----
+        double c_incl = 0.0;
+        float dt_own = 0.f;
+        if (tid < 128) {
+            if (hh + 1 < nh) z_next = raw_delta(h + 1);
+            dt_own = t0 + tid < a.T ? (a.softplus ? ssm_softplus(z) : z) : 0.f;
+            c_incl = ssm_warp_scan((double)a.A[h] * (double)dt_own * 1.4426950408889634074);
+            if (lane == 31) s_cw[warp] = c_incl;
+        }
         __syncthreads();
-        const int h = h0 + hh, set = hh & 1;
-        const size_t unit = ((size_t)b * nch + ch) * a.H + h;  // of the states
-        const double *s_c = s_c2 + set * 128;
-        const float *s_dt = s_dt2 + set * 128;
-        float *s_rowp = s_set + set * L::kSet, *s_colp = s_rowp + 256, *s_diag = s_colp + 512, *s_wd = s_diag + 128,
-              *s_gxp = s_wd + 128, *s_syp = s_gxp + 256;
-        double *s_red = s_red2 + set * 8;
-        {   // tables
-            const double last = s_c[127];
-            if (tid < 128) {
-                const double c = s_c[tid], r = tid >= 32 ? s_c[(tid & ~31) - 1] : 0.0;
-                s_e[tid] = exp2f((float)c);
-                s_rowf[tid] = exp2f((float)(c - r));
-                s_el[tid] = exp2f((float)(last - c));
-                const float hi = (float)c;
-                s_hi[tid] = hi;
-                s_lo[tid] = (float)(c - (double)hi);
-            } else {
-                for (int i = tid - 128; i < 192; i += 128) {
-                    const int I = i < 32 ? 1 : i < 96 ? 2 : 3, j = i < 32 ? i : i < 96 ? i - 32 : i - 96;
-                    s_col[(I - 1) * 96 + j] = exp2f((float)(s_c[32 * I - 1] - s_c[j]));
-                }
+        double c_last = s_cw[0] + s_cw[1] + s_cw[2] + s_cw[3];
+        if (tid < 128) {
+            double r = 0.0;  // c at the end of the block before this token's
+            for (int w = 0; w < warp; ++w) r += s_cw[w];
+            const double c = r + c_incl;
+            s_dt[tid] = dt_own;
+            s_e[tid] = exp2f((float)c);
+            s_rowf[tid] = exp2f((float)c_incl);
+            s_el[tid] = exp2f((float)(c_last - c));
+            const float hi = (float)c;
+            s_hi[tid] = hi;
+            s_lo[tid] = (float)(c - (double)hi);
+            for (int I = warp + 1; I < 4; ++I) {
+                r += s_cw[I - 1];
+                s_col[(I - 1) * 96 + tid] = exp2f((float)(r - c));
             }
         }
         if (tid == 0) {
@@ -221,7 +394,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             if (!mbar_wait(bar_y, (uint32_t)(hh & 1))) *abort_flag = 1;
             else ++d_y;
         }
-        worker_sync();
+        __syncthreads();
         if (*abort_flag) break;
         // ---- W = dY X^T (and once K = C B^T) ----
         if (tid == 0) {
@@ -236,68 +409,64 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         mma_sync_point();
         if (*abort_flag) break;
-        // ---- M' = L K, dK = L W Delta, and the sums of R = M' W ----
+        // ---- M' = L K, dK = L W Delta, and the sums of R = M' W: rows i, 32 columns j ----
         {
-            const float rf = s_rowf[row], ci = s_hi[row], cl = s_lo[row];
+            uint8_t *dm = sm + L::oM + (prt >> 1) * kTile, *dk = sm + L::oK + (prt >> 1) * kTile;
+            const int cc = (prt & 1) * 4;
             float rsum = 0.f;
-#pragma unroll 1
-            for (int jb = 0; jb < 2; ++jb) {
-                const int J = half * 2 + jb;
-                uint8_t *dm = sm + L::oM + half * kTile, *dk = sm + L::oK + half * kTile;
-                if (J > q) {
-                    const uint4 z = make_uint4(0, 0, 0, 0);
+            if (prt > q) {
+                const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        *reinterpret_cast<uint4 *>(dm + sw128_offset(row, jb * 4 + i)) = z;
-                        *reinterpret_cast<uint4 *>(dk + sw128_offset(row, jb * 4 + i)) = z;
-                    }
-                    s_colp[q * 128 + J * 32 + lane] = 0.f;
-                    continue;
+                for (int i = 0; i < 4; ++i) {
+                    *reinterpret_cast<uint4 *>(dm + sw128_offset(row, cc + i)) = zero;
+                    *reinterpret_cast<uint4 *>(dk + sw128_offset(row, cc + i)) = zero;
                 }
+                s_colp[q * 128 + prt * 32 + lane] = 0.f;
+            } else {
                 float kv[32], wv[32], rr[32];
-                tmem_ld32(tl + tK + J * 32, kv);
-                tmem_ld32(tl + tT + J * 32, wv);
-                if (J < q) {
-                    const float *col = s_col + (q - 1) * 96 + J * 32;
+                tmem_ld32(tl + tK + prt * 32, kv);
+                tmem_ld32(tl + tT + prt * 32, wv);
+                if (prt < q) {
+                    const float rf = s_rowf[row];
+                    const float *col = s_col + (q - 1) * 96 + prt * 32;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float l = rf * col[i], d = s_dt[J * 32 + i];
+                        const float l = rf * col[i], d = s_dt[prt * 32 + i];
                         kv[i] *= l;
                         rr[i] = kv[i] * wv[i];
                         rsum = fmaf(rr[i], d, rsum);
                         wv[i] *= l * d;
                     }
                 } else {
+                    const float ci = s_hi[row], cl = s_lo[row];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const int j = J * 32 + i;
-                        const float e = exp2f((ci - s_hi[j]) + (cl - s_lo[j])), l = i <= lane ? e : 0.f, d = s_dt[j];
-                        const float w = wv[i];
+                        const int j = prt * 32 + i;
+                        const float l = exp2f((ci - s_hi[j]) + (cl - s_lo[j])), d = s_dt[j], w = wv[i];
                         kv[i] = i <= lane ? kv[i] * l : 0.f;
                         rr[i] = kv[i] * w;
                         wv[i] = i <= lane ? w * (l * d) : 0.f;
                         if (i == lane) {
                             s_diag[row] = rr[i];
                             s_wd[row] = w;
-                            rr[i] = 0.f;
                         }
-                        if (i > lane) rr[i] = 0.f;
+                        if (i >= lane) rr[i] = 0.f;
                         rsum = fmaf(rr[i], d, rsum);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    st_bf16x8(dm + sw128_offset(row, jb * 4 + i), kv + 8 * i);
-                    st_bf16x8(dk + sw128_offset(row, jb * 4 + i), wv + 8 * i);
+                    st_bf16x8(dm + sw128_offset(row, cc + i), kv + 8 * i);
+                    st_bf16x8(dk + sw128_offset(row, cc + i), wv + 8 * i);
                 }
                 ssm_column_sums(rr);
-                s_colp[q * 128 + J * 32 + lane] = rr[0];
+                s_colp[q * 128 + prt * 32 + lane] = rr[0];
             }
-            s_rowp[half * 128 + row] = rsum;
+            s_rowp[prt * 128 + row] = rsum;
         }
         fence_async_smem();
         tc_before_sync();
-        worker_sync();
+        __syncthreads();
         // ---- the chunk's own products ----
         if (tid == 0) {
             tc_after_sync();
@@ -313,32 +482,72 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 mma_bf16(tmem + tB, desc_mn(sb + L::oK, kk), desc_mn(sb + L::oC, kk), idesc_bf16(128, N, true, true),
                          hh > 0 || kk > 0);
         }
-        float st[kChunks][8], dxi[P / 2];
-        load_state(Sin + unit * P * N, st);
         mma_sync_point();
         if (*abort_flag) break;
-        {
-#pragma unroll
-            for (int c = 0; c < P / 2; c += 32) tmem_ld32(tl + tT + half * (P / 2) + c, dxi + c);
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) st_split8(sm + L::oHi + chunk_off(i), sm + L::oLo + chunk_off(i), st[i]);
-        }
-        fence_async_smem();
+        if (tid == 0) issue_state(&tm_s, unit);  // over M' and dK
+        __syncwarp();
+        float dxi[PW];
+        tmem_ldw<PW>(tl + tT + prt * PW, dxi);
         tc_before_sync();
-        worker_sync();
+        __syncthreads();
         // ---- T = dY S_in ----
+        wait_state();
         if (tid == 0) {
             tc_after_sync();
 #pragma unroll
             for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
                 for (int kk = 0; kk < P / 16; ++kk)
-                    mma_bf16(tmem + tT, desc_k(sb + L::oY, kk), desc_mn(sb + (pt ? L::oLo : L::oHi), kk, L::kSBlock),
-                             idesc_bf16(128, N, false, true), pt > 0 || kk > 0);
+                    mma_bf16(tmem + tT, desc_k(sb + L::oY, kk), desc_k(sb + (pt ? L::oLo : L::oHi), kk, L::kSBlock),
+                             idesc_bf16(128, N, false, false), pt > 0 || kk > 0);
+        }
+        float st[kChunks][8];
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            float lo[8];
+            ld8s(sm + L::oHi + chunk_off(i), st[i]);
+            ld8s(sm + L::oLo + chunk_off(i), lo);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) st[i][e] += lo[e];
+        }
+        mma_sync_point();
+        if (*abort_flag) break;
+        if (tid == 0) issue_state(&tm_g, unit);
+        __syncwarp();
+        {
+            const float e = s_e[row];
+            const int c = prt * NW;
+            float dot = 0.f, t[NW], acc[NW];
+            tmem_ldw<NW>(tl + tT + c, t);
+            tmem_ldw<NW>(tl + tC + c, acc);
+#pragma unroll
+            for (int i = 0; i < NW / 8; ++i) {
+                float v[8];
+                ld8s(sm + L::oC + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) dot = fmaf(v[k], t[8 * i + k], dot);
+            }
+#pragma unroll
+            for (int i = 0; i < NW; ++i) acc[i] = fmaf(e, t[i], acc[i]);
+            tmem_stw<NW>(tl + tC + c, acc);
+            tmem_wait_st();
+            s_syp[prt * 128 + row] = e * dot;
+        }
+        tc_before_sync();
+        __syncthreads();
+        // ---- T = X G_out ----
+        wait_state();
+        if (tid == 0) {
+            tc_after_sync();
+#pragma unroll
+            for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+                for (int kk = 0; kk < P / 16; ++kk)
+                    mma_bf16(tmem + tT, desc_k(sb + L::oX, kk), desc_k(sb + (pt ? L::oLo : L::oHi), kk, L::kSBlock),
+                             idesc_bf16(128, N, false, false), pt > 0 || kk > 0);
         }
         {
-            load_state(Gout + unit * P * N, st);
-            float dot = 0.f;  // <G, S_in>, S_in from its two parts
+            float dot = 0.f;  // <G, S_in>, each from its two parts
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 float x[8], y[8];
@@ -347,112 +556,108 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dot = fmaf(x[e] + y[e], st[i][e], dot);
             }
-            double dd = dot;
-#pragma unroll
-            for (int off = 16; off; off >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, off);
+            const double dd = ssm_warp_sum((double)dot);
             if (lane == 0) s_red[warp] = dd;
         }
         mma_sync_point();
         if (*abort_flag) break;
-        {
-            const float e = s_e[row];
-            float dot = 0.f;
-#pragma unroll 1
-            for (int c = half * (N / 2); c < (half + 1) * (N / 2); c += 32) {
-                float t[32], acc[32];
-                tmem_ld32(tl + tT + c, t);
-                tmem_ld32(tl + tC + c, acc);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v[8];
-                    ld8s(sm + L::oC + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), v);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) dot = fmaf(v[k], t[8 * i + k], dot);
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[i] = fmaf(e, t[i], acc[i]);
-                tmem_st32(tl + tC + c, acc);
-            }
-            tmem_wait_st();
-            s_syp[half * 128 + row] = e * dot;
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) st_split8(sm + L::oHi + chunk_off(i), sm + L::oLo + chunk_off(i), st[i]);
-        }
-        fence_async_smem();
-        tc_before_sync();
-        worker_sync();
-        // ---- T = X G_out ----
-        if (tid == 0) {
-            tc_after_sync();
-#pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-                for (int kk = 0; kk < P / 16; ++kk)
-                    mma_bf16(tmem + tT, desc_k(sb + L::oX, kk), desc_mn(sb + (pt ? L::oLo : L::oHi), kk, L::kSBlock),
-                             idesc_bf16(128, N, false, true), pt > 0 || kk > 0);
-        }
-        mma_sync_point();
-        if (*abort_flag) break;
         if (tid == 0 && hh + 1 < nh) issue_x(h + 1);
+        __syncwarp();
         {
             const float el = s_el[row], w = el * s_dt[row];
-            float dot = 0.f;
-#pragma unroll 1
-            for (int c = half * (N / 2); c < (half + 1) * (N / 2); c += 32) {
-                float t[32], acc[32];
-                tmem_ld32(tl + tT + c, t);
-                tmem_ld32(tl + tB + c, acc);
+            const int c = prt * NW;
+            float dot = 0.f, t[NW], acc[NW];
+            tmem_ldw<NW>(tl + tT + c, t);
+            tmem_ldw<NW>(tl + tB + c, acc);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v[8];
-                    ld8s(sm + L::oB + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), v);
+            for (int i = 0; i < NW / 8; ++i) {
+                float v[8];
+                ld8s(sm + L::oB + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), v);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) dot = fmaf(v[k], t[8 * i + k], dot);
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[i] = fmaf(w, t[i], acc[i]);
-                tmem_st32(tl + tB + c, acc);
+                for (int k = 0; k < 8; ++k) dot = fmaf(v[k], t[8 * i + k], dot);
             }
+#pragma unroll
+            for (int i = 0; i < NW; ++i) acc[i] = fmaf(w, t[i], acc[i]);
+            tmem_stw<NW>(tl + tB + c, acc);
             tmem_wait_st();
-            s_gxp[half * 128 + row] = el * dot;
+            s_gxp[prt * 128 + row] = el * dot;
         }
         tc_before_sync();
-        worker_sync();
-        // ---- T = B G_out^T ----
+        __syncthreads();
+        // ---- T = B G_out^T; beside it the per-token sums of this head: token tid ----
         if (tid == 0) {
             tc_after_sync();
 #pragma unroll
             for (int kk = 0; kk < N / 16; ++kk)
-                mma_bf16(tmem + tT, desc_k(sb + L::oB, kk), desc_k(sb + L::oHi, kk, L::kSBlock), idesc_bf16(128, P, false, false),
+                mma_bf16(tmem + tT, desc_k(sb + L::oB, kk), desc_mn(sb + L::oHi, kk, L::kSBlock), idesc_bf16(128, P, false, true),
                          kk > 0);
+        }
+        double pre = 0.0, suf = 0.0, pre_in = 0.0, suf_in = 0.0, own = 0.0;
+        if (tid < 128) {
+            const double col = (double)s_colp[tid] + (double)s_colp[128 + tid] + (double)s_colp[256 + tid] + (double)s_colp[384 + tid];
+            const double gx = (double)s_gxp[tid] + (double)s_gxp[128 + tid] + (double)s_gxp[256 + tid] + (double)s_gxp[384 + tid];
+            const double rw = (double)s_rowp[tid] + (double)s_rowp[128 + tid] + (double)s_rowp[256 + tid] + (double)s_rowp[384 + tid];
+            suf = (double)s_syp[tid] + (double)s_syp[128 + tid] + (double)s_syp[256 + tid] + (double)s_syp[384 + tid];
+            own = col + (double)s_diag[tid] + gx;
+            pre = (double)s_dt[tid] * (col + gx) - rw;
+            pre_in = ssm_warp_scan(pre);
+            suf_in = ssm_warp_scan(suf);
+            if (lane == 31) {
+                s_tw[warp] = pre_in;
+                s_tw[4 + warp] = suf_in;
+            }
         }
         mma_sync_point();
         if (*abort_flag) break;
-        // ---- dx over dY ----
+        // ---- dx over dY, and the end of the token sums ----
         {
             const float el = s_el[row], dt = s_dt[row], D = a.D ? a.D[h] : 0.f;
+            const int c = prt * PW;
+            float t[PW];
+            tmem_ldw<PW>(tl + tT + c, t);
 #pragma unroll
-            for (int cc = 0; cc < P / 2; cc += 32) {
-                const int c = half * (P / 2) + cc;
-                float t[32];
-                tmem_ld32(tl + tT + c, t);
+            for (int i = 0; i < PW / 8; ++i) {
+                uint8_t *p = sm + L::oY + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i);
+                float y[8];
+                ld8s(p, y);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint8_t *p = sm + L::oY + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i);
-                    float y[8];
-                    ld8s(p, y);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float v = dt * fmaf(el, t[8 * i + k], dxi[cc + 8 * i + k]);
-                        y[k] = a.D ? fmaf(D, y[k], v) : v;
-                    }
-                    st_bf16x8(p, y);
+                for (int k = 0; k < 8; ++k) {
+                    const float v = dt * fmaf(el, t[8 * i + k], dxi[8 * i + k]);
+                    y[k] = a.D ? fmaf(D, y[k], v) : v;
                 }
+                st_bf16x8(p, y);
+            }
+        }
+        if (tid < 128) {
+            double cross = 0.0, before = pre_in - pre, after = -(suf_in - suf);
+            for (int w = 0; w < 16; ++w) cross += s_red[w];
+            for (int w = 0; w < 4; ++w) {
+                if (w < warp) before += s_tw[w];
+                if (w >= warp) after += s_tw[4 + w];
+            }
+            const double Ah = (double)a.A[h], dlog = before + after + cross * exp2(c_last);
+            double raw = own + Ah * dlog, sA = 0.0, sD = 0.0;
+            if (a.softplus) raw *= 1.0 / (1.0 + exp(-(double)z));
+            if (tid < valid) {
+                a.ddelta[((size_t)b * a.T + t0 + tid) * a.H + h] = (float)raw;
+                sA = (double)dt_own * dlog;
+                sD = (double)s_wd[tid];
+            } else {
+                raw = 0.0;
+            }
+            sA = ssm_warp_sum(sA);
+            raw = ssm_warp_sum(raw);
+            sD = ssm_warp_sum(sD);
+            if (lane == 0) {
+                s_tot[warp * 3] = sA;
+                s_tot[warp * 3 + 1] = raw;
+                s_tot[warp * 3 + 2] = sD;
             }
         }
         fence_async_smem();
         tc_before_sync();
-        worker_sync();
+        __syncthreads();
+        if (tid < 3) part[tid * units + unit] = (float)(s_tot[tid] + s_tot[3 + tid] + s_tot[6 + tid] + s_tot[9 + tid]);
         if (tid == 0) {
             for (int i = 0; i < P / 64; ++i) tma_store_4d(&tm_dx, sm + L::oY + i * kTile, i * 64, h, t0, b);
             bulk_commit();
@@ -460,38 +665,34 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             if (hh + 1 < nh) issue_y(h + 1);
         }
     }
-    if (worker) __syncthreads();  // the last head's sums (or, given up, the meeting that warp 8 still waits at)
     if (*abort_flag) {
         if (tid == 0) {
             record_status(GDR_ERR_TIMEOUT);
             if (bc_open) mbar_wait(bar_bc, 0);
             if (d_x < n_x) mbar_wait(bar_x, (uint32_t)(d_x & 1));
             if (d_y < n_y) mbar_wait(bar_y, (uint32_t)(d_y & 1));
+            if (n_s > 0) mbar_wait(bar_s, (uint32_t)((n_s - 1) & 1));
             if (mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
             bulk_wait_all();
         }
     } else {
         tc_after_sync();
-        if (worker) {
-            const bool on = row < valid;
-            const size_t at = (((size_t)b * a.T + t0 + row) * a.G + g);
+        const bool on = row < valid;
+        const size_t at = (((size_t)b * a.T + t0 + row) * a.G + g);
+        const int c = prt * NW;
 #pragma unroll 1
-            for (int which = 0; which < 2; ++which) {
-#pragma unroll 1
-                for (int c = half * (N / 2); c < (half + 1) * (N / 2); c += 32) {
-                    float v[32];
-                    tmem_ld32(tl + (which ? tB : tC) + c, v);
-                    if (!on) continue;
-                    if (splits == 1) {
-                        uint8_t *dst = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(which ? a.dB : a.dC) + at * N + c);
+        for (int which = 0; which < 2; ++which) {
+            float v[NW];
+            tmem_ldw<NW>(tl + (which ? tB : tC) + c, v);
+            if (!on) continue;
+            if (splits == 1) {
+                uint8_t *dst = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(which ? a.dB : a.dC) + at * N + c);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) st_bf16x8(dst + 16 * i, v + 8 * i);
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>((which ? dBp : dCp) + (at * splits + sp) * N + c);
+                for (int i = 0; i < NW / 8; ++i) st_bf16x8(dst + 16 * i, v + 8 * i);
+            } else {
+                float4 *dst = reinterpret_cast<float4 *>((which ? dBp : dCp) + (at * splits + sp) * N + c);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    }
-                }
+                for (int i = 0; i < NW / 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
         }
         if (tid == 0) bulk_wait_all();
@@ -505,15 +706,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
 }
 
 // ---- host side ------------------------------------------------------------------------------
-// CTAs per group of heads: the fewest heads in a row for the SMs, one CTA where that is as good.
+// CTAs per group of heads: a CTA costs about half a head's time beside its heads (C B^T, the first loads, dB and dC).
 inline int ssm_grad_splits(int B, int T, int H, int G) {
     const int nch = (T + kTcQ - 1) / kTcQ, HG = H / G, sms = ssm_sm_count();
     int best = 1;
-    long long cost = -1;
+    double cost = -1;
     for (int s = 1; s <= HG; ++s) {
         const int per = (HG + s - 1) / s;
         if ((HG + per - 1) / per != s) continue;
-        const long long c = (((long long)B * nch * G * s + sms - 1) / sms) * per;
+        const double c = (double)(((long long)B * nch * G * s + sms - 1) / sms) * (per + (s > 1 ? 1.0 : 0.5));
         if (cost < 0 || c < cost) {
             cost = c;
             best = s;
@@ -522,18 +723,42 @@ inline int ssm_grad_splits(int B, int T, int H, int G) {
     return best;
 }
 
+// Chunks per segment of the walk: rounds of chunks over the SMs' places (two a SM, both directions, halves of P);
+// a cut costs the segments' own states (as much again without the writes) and two launches.
+inline int ssm_walk_chunks(int B, int T, int H, int P) {
+    const int nch = (T + kTcQ - 1) / kTcQ, places = ssm_sm_count() * 2;
+    double best = 1e30;
+    int at = nch;
+    for (int m = nch; m >= 1; m = m > 64 ? m * 3 / 4 : m - 1) {
+        const int R = (nch + m - 1) / m;
+        const double rounds = (double)((2LL * (P / 64) * B * H * R + places - 1) / places);
+        const double cost = R == 1 ? rounds * m : rounds * (2.0 * m + 1.0) + 6.0;
+        if (cost < best * 0.999) {
+            best = cost;
+            at = m;
+        }
+    }
+    return at;
+}
+
 struct SsmTcBwdWs {
-    size_t st, g, dec, part, dBp, dCp, total;
-    int splits;
+    size_t st, g, segS, segG, dec, part, dBp, dCp, total;
+    int splits, m, R;
 };
 inline SsmTcBwdWs ssm_tc_bwd_ws(int B, int T, int H, int G, int P, int N) {
-    const size_t units = (size_t)B * ((T + kTcQ - 1) / kTcQ) * H;
+    const int nch = (T + kTcQ - 1) / kTcQ;
+    const size_t units = (size_t)B * nch * H;
     SsmTcBwdWs w;
     w.splits = ssm_grad_splits(B, T, H, G);
+    w.m = ssm_walk_chunks(B, T, H, P);
+    w.R = (nch + w.m - 1) / w.m;
+    const size_t segs = w.R > 1 ? (size_t)B * w.R * H : 0;
     w.st = 0;
     w.g = ssm_align(units * P * N * 4);
-    w.dec = 2 * w.g;
-    w.part = w.dec + ssm_align(units * 4);
+    w.segS = 2 * w.g;
+    w.segG = w.segS + ssm_align(segs * P * N * 4);
+    w.dec = w.segG + ssm_align(segs * P * N * 4);
+    w.part = w.dec + ssm_align(segs * 4);
     w.dBp = w.part + ssm_align(3 * units * 4);
     const size_t p = w.splits > 1 ? ssm_align((size_t)B * T * G * w.splits * N * 4) : 0;
     w.dCp = w.dBp + p;
@@ -543,29 +768,39 @@ inline SsmTcBwdWs ssm_tc_bwd_ws(int B, int T, int H, int G, int P, int N) {
 
 template <int P, int N>
 cudaError_t ssm_tc_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
-    CUtensorMap mx, mb, mc, my, mdx;
-    if (!ssm_token_map(&mx, a.x, a.B, a.T, a.H, P, a.ldx) || !ssm_token_map(&mb, a.Bm, a.B, a.T, a.G, N, a.ldb) ||
-        !ssm_token_map(&mc, a.Cm, a.B, a.T, a.G, N, a.ldc) || !ssm_token_map(&my, a.dy, a.B, a.T, a.H, P, a.H * P) ||
-        !ssm_token_map(&mdx, a.dx, a.B, a.T, a.H, P, a.H * P))
-        return cudaErrorInvalidValue;
+    const int nch = (a.T + kTcQ - 1) / kTcQ;
     const SsmTcBwdWs w = ssm_tc_bwd_ws(a.B, a.T, a.H, a.G, P, N);
-    const int nch = (a.T + kTcQ - 1) / kTcQ, HG = a.H / a.G, per = (HG + w.splits - 1) / w.splits;
     uint8_t *base = static_cast<uint8_t *>(ws);
-    float *st = reinterpret_cast<float *>(base + w.st), *g = reinterpret_cast<float *>(base + w.g);
+    __nv_bfloat16 *st = reinterpret_cast<__nv_bfloat16 *>(base + w.st), *g = reinterpret_cast<__nv_bfloat16 *>(base + w.g);
+    float *segS = reinterpret_cast<float *>(base + w.segS), *segG = reinterpret_cast<float *>(base + w.segG);
     float *dec = reinterpret_cast<float *>(base + w.dec), *part = reinterpret_cast<float *>(base + w.part);
     float *dBp = reinterpret_cast<float *>(base + w.dBp), *dCp = reinterpret_cast<float *>(base + w.dCp);
-    const dim3 grid((unsigned)(a.B * a.H) * (unsigned)nch);
-    cudaError_t e = ssm_launch(ssm_tc_state_kernel<P, N, false>, grid, 256, (size_t)SsmStateTc<P, N, false>::kAlloc, s, mx, mb,
-                               a, 1, st, dec);
+    const size_t units = (size_t)a.B * nch * a.H;
+    CUtensorMap mx, mb, mc, my, mdx, ms, mg;
+    if (!ssm_token_map(&mx, a.x, a.B, a.T, a.H, P, a.ldx) || !ssm_token_map(&mb, a.Bm, a.B, a.T, a.G, N, a.ldb) ||
+        !ssm_token_map(&mc, a.Cm, a.B, a.T, a.G, N, a.ldc) || !ssm_token_map(&my, a.dy, a.B, a.T, a.H, P, a.H * P) ||
+        !ssm_token_map(&mdx, a.dx, a.B, a.T, a.H, P, a.H * P) || !ssm_state_map(&ms, st, units, P, N) ||
+        !ssm_state_map(&mg, g, units, P, N))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaSuccess;
+    if (w.R > 1) {
+        const dim3 grid((unsigned)(a.B * a.H) * (unsigned)w.R);
+        e = ssm_launch(ssm_tc_state_kernel<P, N, false>, grid, 256, (size_t)SsmStateTc<P, N, false>::kAlloc, s, mx, mb, a, w.m,
+                       segS, dec);
+        if (e == cudaSuccess)
+            e = ssm_launch(ssm_tc_state_kernel<P, N, true>, grid, 256, (size_t)SsmStateTc<P, N, true>::kAlloc, s, my, mc, a,
+                           w.m, segG, dec);
+        if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, w.R, a.H, P * N, segS, dec, a.S0, nullptr, s);
+        if (e == cudaSuccess) e = ssm_launch_scan(true, a.B, w.R, a.H, P * N, segG, dec, a.dS_T, nullptr, s);
+    }
     if (e == cudaSuccess)
-        e = ssm_launch(ssm_tc_state_kernel<P, N, true>, grid, 256, (size_t)SsmStateTc<P, N, true>::kAlloc, s, my, mc, a, 1, g,
-                       dec);
-    if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, nch, a.H, P * N, st, dec, a.S0, nullptr, s);
-    if (e == cudaSuccess) e = ssm_launch_scan(true, a.B, nch, a.H, P * N, g, dec, a.dS_T, a.dS0, s);
+        e = ssm_launch(ssm_tc_walk_kernel<P, N>, dim3(2u * (P / 64) * (unsigned)(a.B * a.H) * (unsigned)w.R), 256,
+                       (size_t)SsmWalkTc<N>::kAlloc, s, mx, mb, my, mc, a, w.m, (const float *)segS, (const float *)segG, st, g);
+    const int per = (a.H / a.G + w.splits - 1) / w.splits;
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_grad_kernel<P, N>, dim3((unsigned)((size_t)a.B * nch * a.G * w.splits)), kGradThreads,
-                       (size_t)SsmGradTc<P, N>::kAlloc, s, mx, mb, mc, my, mdx, a, w.splits, per, (const float *)st,
-                       (const float *)g, dBp, dCp, part);
+                       (size_t)SsmGradTc<P, N>::kAlloc, s, mx, mb, mc, my, mdx, ms, mg, a, w.splits, per,
+                       (const __nv_bfloat16 *)st, (const __nv_bfloat16 *)g, dBp, dCp, part);
     if (e != cudaSuccess) return e;
     if (w.splits > 1) {
         const long long total4 = (long long)a.B * a.T * a.G * (N / 4);

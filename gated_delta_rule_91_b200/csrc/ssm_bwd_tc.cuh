@@ -44,25 +44,25 @@ struct SsmWalkTc {
     static constexpr uint32_t BB = N / 64 * kTile;
     static constexpr uint32_t oX = 0, oHi = kTile, oLo = oHi + BB, oZero = oLo + BB;
     static constexpr uint32_t kHiBlock = N == 64 ? 2 * kTile : kTile;
-    static constexpr uint32_t oCtl = oZero + (N == 64 ? kTile : 0);
-    static constexpr uint32_t kAlloc = oCtl + 2 * 128 * 12 + 128 + 1024;
+    static constexpr uint32_t oGate = oZero + (N == 64 ? kTile : 0);  // two tables
+    static constexpr uint32_t oCtl = oGate + 2 * SsmGate::kFwdBytes;
+    static constexpr uint32_t kAlloc = oCtl + 64 + 1024;
 };
 
 template <int P, int N>
 __global__ void __launch_bounds__(256, 2) ssm_tc_walk_kernel(
     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
     const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_c, SsmArgs a, int m,
-    const float *__restrict__ seg_S, const float *__restrict__ seg_G, __nv_bfloat16 *__restrict__ out_S,
+    const float *__restrict__ gates, const float *__restrict__ seg_S, const float *__restrict__ seg_G,
+    __nv_bfloat16 *__restrict__ out_S,
     __nv_bfloat16 *__restrict__ out_G) {
     using L = SsmWalkTc<N>;
     using namespace sm100;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
-    double *s_c2 = reinterpret_cast<double *>(sm + L::oCtl);
-    float *s_dt2 = reinterpret_cast<float *>(s_c2 + 256);
-    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(s_dt2 + 256), *mma_bar = tma_bar + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tma_bar + 2);
+    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(sm + L::oCtl), *mma_bar = tma_bar + 1, *bar_g = tma_bar + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tma_bar + 3);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(256, 2) ssm_tc_walk_kernel(
     if (tid == 0) {
         mbar_init(tma_bar, 1);
         mbar_init(mma_bar, 1);
+        mbar_init(bar_g, 1);
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -96,8 +97,16 @@ __global__ void __launch_bounds__(256, 2) ssm_tc_walk_kernel(
         for (int i = 0; i < N / 64; ++i)
             tma_load_4d(sm + L::oHi + i * kTile, rev ? &tm_c : &tm_b, tma_bar, i * 64, g, chunk(k) * kTcQ, b);
     };
-    if (tid == 0) issue(0);
-    if (warp == 1) ssm_tc_gates(a, b, h, chunk(0) * kTcQ, s_dt2, s_c2);
+    auto issue_g = [&](int k) {
+        mbar_expect_tx(bar_g, SsmGate::kFwdBytes);
+        bulk_load_g2s(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes,
+                      gates + (((size_t)b * nch + chunk(k)) * a.H + h) * SsmGate::stride, SsmGate::kFwdBytes, bar_g);
+    };
+    int n_x = 1, n_g = 1;
+    if (tid == 0) {
+        issue_g(0);
+        issue(0);
+    }
     float v[32];
     {
         const float *src = R > 1 ? (rev ? seg_G : seg_S) + (((size_t)b * R + seg) * a.H + h) * P * N
@@ -108,16 +117,14 @@ __global__ void __launch_bounds__(256, 2) ssm_tc_walk_kernel(
         tmem_st32(tl, v);
         tmem_wait_st();
     }
-    __syncthreads();
     bool pending = false;
     int k = 0;
 #pragma unroll 1
     for (; k < cn; ++k) {
-        const double *s_c = s_c2 + (k & 1) * 128;
-        const float *s_dt = s_dt2 + (k & 1) * 128;
-        const double last = s_c[127];
+        const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes);
+        if (!mbar_wait(bar_g, (uint32_t)(k & 1))) *abort_flag = 1;  // every thread
         if (row < N) {  // the state as it enters, and its decay
-            const float el = exp2f((float)last);
+            const float el = s_g[SsmGate::elast];
             const size_t unit = ((size_t)b * nch + chunk(k)) * a.H + h;
             uint8_t *hi = reinterpret_cast<uint8_t *>((rev ? out_G : out_S) + ((unit * 2) * N + row) * P + p0 + half * 32);
             uint8_t *lo = hi + (size_t)N * P * 2;
@@ -132,9 +139,14 @@ __global__ void __launch_bounds__(256, 2) ssm_tc_walk_kernel(
         if (tid == 0 && !mbar_wait(tma_bar, (uint32_t)(k & 1))) *abort_flag = 1;
         __syncthreads();
         if (*abort_flag || last_one) break;
+        if (tid == 0 && k + 1 < cn) {  // the other table was last read a chunk ago
+            issue_g(k + 1);
+            ++n_g;
+        }
+        __syncwarp();
         {
             const int r = tid & 127, hf = tid >> 7;
-            const float w = rev ? exp2f((float)s_c[r]) : s_dt[r] * exp2f((float)(last - s_c[r]));
+            const float w = rev ? s_g[SsmGate::e + r] : s_g[SsmGate::dt + r] * s_g[SsmGate::el + r];
             constexpr int CH = N / 16;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -160,14 +172,13 @@ __global__ void __launch_bounds__(256, 2) ssm_tc_walk_kernel(
                              desc_mn(sb + L::oX, kk), idesc_bf16(128, 64, true, true), 1);
             mma_commit(mma_bar);
         }
-        if (warp == 1 && k + 1 < cn)
-            ssm_tc_gates(a, b, h, chunk(k + 1) * kTcQ, s_dt2 + ((k + 1) & 1) * 128, s_c2 + ((k + 1) & 1) * 128);
         if (tid == 0) {
             if (!mbar_wait(mma_bar, (uint32_t)(k & 1))) {
                 *abort_flag = 1;
                 pending = true;
             } else if (k + 1 < cn) {
                 issue(k + 1);
+                ++n_x;
             }
         }
         __syncthreads();
@@ -178,7 +189,9 @@ __global__ void __launch_bounds__(256, 2) ssm_tc_walk_kernel(
     if (*abort_flag) {
         if (tid == 0) {
             record_status(GDR_ERR_TIMEOUT);
-            mbar_wait(pending ? mma_bar : tma_bar, (uint32_t)(k & 1));
+            if (pending) mbar_wait(mma_bar, (uint32_t)(k & 1));
+            mbar_wait(tma_bar, (uint32_t)((n_x - 1) & 1));
+            mbar_wait(bar_g, (uint32_t)((n_g - 1) & 1));
         }
     } else if (rev && seg == 0 && a.dS0 && row < N) {
 #pragma unroll
@@ -201,10 +214,10 @@ struct SsmGradTc {
     static constexpr uint32_t oM = oR, oK = oR + 2 * kTile;   // M', dK
     static constexpr uint32_t oHi = oR, oLo = oR + SB;        // S_in, then G_out
     static constexpr uint32_t oGate = oR + 4 * kTile;
-    // doubles: warp sums of c [4], of the token sums [4][2], totals [4][3], <G, S> [16]; floats dt, e, row, el, hi, lo
-    // [128], col[288], rowp[4][128], colp[4][128], diag, wd, gxp[4][128], syp[4][128]
-    static constexpr uint32_t kGate = (4 + 8 + 12 + 16) * 8 + (6 * 128 + 288 + 18 * 128) * 4;
-    static constexpr uint32_t oBar = oGate + kGate;
+    // two tables; doubles: warp sums of the token sums [4][2], totals [4][3], <G, S> [16]; floats rowp[4][128],
+    // colp[4][128], diag, wd, gxp[4][128], syp[4][128]
+    static constexpr uint32_t oSum = oGate + 2 * SsmGate::kBytes;
+    static constexpr uint32_t oBar = oSum + (8 + 12 + 16) * 8 + 18 * 128 * 4;
     static constexpr uint32_t kAlloc = oBar + 64 + 1024;
 };
 
@@ -242,8 +255,8 @@ template <int P, int N>
 __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_dy,
-    const __grid_constant__ CUtensorMap tm_dx, const __grid_constant__ CUtensorMap tm_s,
-    const __grid_constant__ CUtensorMap tm_g, SsmArgs a, int splits, int per, const __nv_bfloat16 *__restrict__ Sin,
+    const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_g, SsmArgs a, int splits, int per,
+    const float *__restrict__ gates, const __nv_bfloat16 *__restrict__ Sin,
     const __nv_bfloat16 *__restrict__ Gout, float *__restrict__ dBp, float *__restrict__ dCp, float *__restrict__ part) {
     using L = SsmGradTc<P, N>;
     using namespace sm100;
@@ -251,14 +264,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
-    double *s_cw = reinterpret_cast<double *>(sm + L::oGate), *s_tw = s_cw + 4, *s_tot = s_tw + 8, *s_red = s_tot + 12;
-    float *s_dt = reinterpret_cast<float *>(s_red + 16);
-    float *s_e = s_dt + 128, *s_rowf = s_e + 128, *s_el = s_rowf + 128, *s_hi = s_el + 128, *s_lo = s_hi + 128;
-    float *s_col = s_lo + 128, *s_rowp = s_col + 288, *s_colp = s_rowp + 512, *s_diag = s_colp + 512, *s_wd = s_diag + 128,
+    double *s_tw = reinterpret_cast<double *>(sm + L::oSum), *s_tot = s_tw + 8, *s_red = s_tot + 12;
+    float *s_rowp = reinterpret_cast<float *>(s_red + 16), *s_colp = s_rowp + 512, *s_diag = s_colp + 512, *s_wd = s_diag + 128,
           *s_gxp = s_wd + 128, *s_syp = s_gxp + 512;
     uint64_t *bar_bc = reinterpret_cast<uint64_t *>(sm + L::oBar), *bar_x = bar_bc + 1, *bar_y = bar_bc + 2,
-             *bar_s = bar_bc + 3, *mma_bar = bar_bc + 4;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_bc + 5);
+             *bar_s = bar_bc + 3, *bar_g = bar_bc + 4, *mma_bar = bar_bc + 5;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_bc + 6);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = warp & 3, prt = warp >> 2, row = q * 32 + lane;  // TMEM lane, column quarter
@@ -278,6 +289,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         mbar_init(bar_x, 1);
         mbar_init(bar_y, 1);
         mbar_init(bar_s, 1);
+        mbar_init(bar_g, 1);
         mbar_init(mma_bar, 1);
         fence_mbar_init();
         *abort_flag = 0;
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     constexpr uint32_t tK = 0, tT = 128, tC = 256, tB = 256 + N;
 
-    int n_x = 0, n_y = 0, n_s = 0, d_x = 0, d_y = 0;  // thread 0's
+    int n_x = 0, n_y = 0, n_s = 0, n_g = 0;  // issued, by thread 0
     uint32_t s_phase = 0;                             // everyone's
     bool bc_open = false, mma_open = false;
     auto issue_x = [&](int h) {
@@ -310,6 +322,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 tma_load_4d(sm + L::oHi + pt * L::SB + i * L::kSBlock, map, bar_s, i * 64, 0, pt, (int)unit);
         ++n_s;
     };
+    auto issue_g = [&](int hh) {
+        mbar_expect_tx(bar_g, SsmGate::kBytes);
+        bulk_load_g2s(sm + L::oGate + (hh & 1) * SsmGate::kBytes, gates + (unit0 + h0 + hh) * SsmGate::stride, SsmGate::kBytes,
+                      bar_g);
+        ++n_g;
+    };
     auto wait_state = [&] {  // every thread
         if (!mbar_wait(bar_s, s_phase)) *abort_flag = 1;
         s_phase ^= 1;
@@ -323,6 +341,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         bc_open = true;
         issue_x(h0);
         issue_y(h0);
+        issue_g(0);
     }
     uint32_t mma_phase = 0;
     auto mma_sync_point = [&]() {
@@ -341,61 +360,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         const int n = (i * kGradThreads + tid) / (P / 8), p8 = (i * kGradThreads + tid) % (P / 8);
         return (uint32_t)(p8 >> 3) * L::kSBlock + sw128_offset(n, p8 & 7);
     };
-    auto raw_delta = [&](int h) {
-        float z = t0 + tid < a.T ? a.delta[((size_t)b * a.T + t0 + tid) * a.H + h] : 0.f;
-        if (a.bias) z += a.bias[h];
-        return z;
-    };
-    float z_next = tid < 128 ? raw_delta(h0) : 0.f;
-
 #pragma unroll 1
     for (int hh = 0; hh < nh; ++hh) {
         const int h = h0 + hh;
         const size_t unit = unit0 + h;
-        const float z = z_next;
+        const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (hh & 1) * SsmGate::kBytes);
+        const float *s_dt = s_g + SsmGate::dt;
         if (tid < 2 * P * N * 2 / 128) {  // this head's states on their way into L2: a line of each a thread
             prefetch_l2(reinterpret_cast<const uint8_t *>(Sin) + unit * 4 * P * N + tid * 128);
             prefetch_l2(reinterpret_cast<const uint8_t *>(Gout) + unit * 4 * P * N + tid * 128);
-        }
-        // ---- gates: token tid ----
-        double c_incl = 0.0;
-        float dt_own = 0.f;
-        if (tid < 128) {
-            if (hh + 1 < nh) z_next = raw_delta(h + 1);
-            dt_own = t0 + tid < a.T ? (a.softplus ? ssm_softplus(z) : z) : 0.f;
-            c_incl = ssm_warp_scan((double)a.A[h] * (double)dt_own * 1.4426950408889634074);
-            if (lane == 31) s_cw[warp] = c_incl;
-        }
-        __syncthreads();
-        double c_last = s_cw[0] + s_cw[1] + s_cw[2] + s_cw[3];
-        if (tid < 128) {
-            double r = 0.0;  // c at the end of the block before this token's
-            for (int w = 0; w < warp; ++w) r += s_cw[w];
-            const double c = r + c_incl;
-            s_dt[tid] = dt_own;
-            s_e[tid] = exp2f((float)c);
-            s_rowf[tid] = exp2f((float)c_incl);
-            s_el[tid] = exp2f((float)(c_last - c));
-            const float hi = (float)c;
-            s_hi[tid] = hi;
-            s_lo[tid] = (float)(c - (double)hi);
-            for (int I = warp + 1; I < 4; ++I) {
-                r += s_cw[I - 1];
-                s_col[(I - 1) * 96 + tid] = exp2f((float)(r - c));
-            }
         }
         if (tid == 0) {
             if (bc_open) {
                 if (!mbar_wait(bar_bc, 0)) *abort_flag = 1;
                 else bc_open = false;
             }
-            if (!mbar_wait(bar_x, (uint32_t)(hh & 1))) *abort_flag = 1;
-            else ++d_x;
-            if (!mbar_wait(bar_y, (uint32_t)(hh & 1))) *abort_flag = 1;
-            else ++d_y;
+            if (!mbar_wait(bar_g, (uint32_t)(hh & 1)) || !mbar_wait(bar_x, (uint32_t)(hh & 1)) ||
+                !mbar_wait(bar_y, (uint32_t)(hh & 1)))
+                *abort_flag = 1;
         }
         __syncthreads();
         if (*abort_flag) break;
+        if (tid == 0 && hh + 1 < nh) issue_g(hh + 1);  // the other table was last read a head ago
+        __syncwarp();
         // ---- W = dY X^T (and once K = C B^T) ----
         if (tid == 0) {
             tc_after_sync();
@@ -409,11 +396,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         mma_sync_point();
         if (*abort_flag) break;
-        // ---- M' = L K, dK = L W Delta, and the sums of R = M' W: rows i, 32 columns j ----
+        // ---- M' = L K and dK = L W Delta: rows i, 32 columns j; R = M' W stays for the sums below ----
+        float rr[32], rsum = 0.f;
         {
             uint8_t *dm = sm + L::oM + (prt >> 1) * kTile, *dk = sm + L::oK + (prt >> 1) * kTile;
             const int cc = (prt & 1) * 4;
-            float rsum = 0.f;
             if (prt > q) {
                 const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -421,48 +408,61 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                     *reinterpret_cast<uint4 *>(dm + sw128_offset(row, cc + i)) = zero;
                     *reinterpret_cast<uint4 *>(dk + sw128_offset(row, cc + i)) = zero;
                 }
-                s_colp[q * 128 + prt * 32 + lane] = 0.f;
             } else {
-                float kv[32], wv[32], rr[32];
+                float kv[32], wv[32];
+                const float4 *dt4 = reinterpret_cast<const float4 *>(s_dt + prt * 32);
                 tmem_ld32(tl + tK + prt * 32, kv);
                 tmem_ld32(tl + tT + prt * 32, wv);
                 if (prt < q) {
-                    const float rf = s_rowf[row];
-                    const float *col = s_col + (q - 1) * 96 + prt * 32;
+                    const float rf = s_g[SsmGate::rowf + row];
+                    const float4 *col4 = reinterpret_cast<const float4 *>(s_g + SsmGate::col + (q - 1) * 96 + prt * 32);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float l = rf * col[i], d = s_dt[prt * 32 + i];
-                        kv[i] *= l;
-                        rr[i] = kv[i] * wv[i];
-                        rsum = fmaf(rr[i], d, rsum);
-                        wv[i] *= l * d;
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 c4 = col4[i], d4 = dt4[i];
+                        const float l[4] = {rf * c4.x, rf * c4.y, rf * c4.z, rf * c4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int n = 4 * i + u;
+                            kv[n] *= l[u];
+                            rr[n] = kv[n] * wv[n];
+                            rsum = fmaf(rr[n], d[u], rsum);
+                            wv[n] *= l[u] * d[u];
+                        }
                     }
                 } else {
-                    const float ci = s_hi[row], cl = s_lo[row];
+                    const float ci = s_g[SsmGate::hi + row], cl = s_g[SsmGate::lo + row];
+                    const float4 *hi4 = reinterpret_cast<const float4 *>(s_g + SsmGate::hi + prt * 32);
+                    const float4 *lo4 = reinterpret_cast<const float4 *>(s_g + SsmGate::lo + prt * 32);
+                    float dg = 0.f, wd = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int j = prt * 32 + i;
-                        const float l = exp2f((ci - s_hi[j]) + (cl - s_lo[j])), d = s_dt[j], w = wv[i];
-                        kv[i] = i <= lane ? kv[i] * l : 0.f;
-                        rr[i] = kv[i] * w;
-                        wv[i] = i <= lane ? w * (l * d) : 0.f;
-                        if (i == lane) {
-                            s_diag[row] = rr[i];
-                            s_wd[row] = w;
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 h4 = hi4[i], l4 = lo4[i], d4 = dt4[i];
+                        const float l[4] = {exp2f((ci - h4.x) + (cl - l4.x)), exp2f((ci - h4.y) + (cl - l4.y)),
+                                            exp2f((ci - h4.z) + (cl - l4.z)), exp2f((ci - h4.w) + (cl - l4.w))};
+                        const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int n = 4 * i + u;
+                            const float w = wv[n], r = kv[n] * l[u] * w;
+                            if (n == lane) {
+                                dg = r;
+                                wd = w;
+                            }
+                            kv[n] = n <= lane ? kv[n] * l[u] : 0.f;
+                            wv[n] = n <= lane ? w * (l[u] * d[u]) : 0.f;
+                            rr[n] = n < lane ? r : 0.f;
+                            rsum = fmaf(rr[n], d[u], rsum);
                         }
-                        if (i >= lane) rr[i] = 0.f;
-                        rsum = fmaf(rr[i], d, rsum);
                     }
+                    s_diag[row] = dg;
+                    s_wd[row] = wd;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     st_bf16x8(dm + sw128_offset(row, cc + i), kv + 8 * i);
                     st_bf16x8(dk + sw128_offset(row, cc + i), wv + 8 * i);
                 }
-                ssm_column_sums(rr);
-                s_colp[q * 128 + prt * 32 + lane] = rr[0];
             }
-            s_rowp[prt * 128 + row] = rsum;
         }
         fence_async_smem();
         tc_before_sync();
@@ -482,12 +482,31 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 mma_bf16(tmem + tB, desc_mn(sb + L::oK, kk), desc_mn(sb + L::oC, kk), idesc_bf16(128, N, true, true),
                          hh > 0 || kk > 0);
         }
+        __syncwarp();
+        if (prt <= q) {  // the sums of R, beside the products
+            ssm_column_sums(rr);
+            s_colp[q * 128 + prt * 32 + lane] = rr[0];
+        } else {
+            s_colp[q * 128 + prt * 32 + lane] = 0.f;
+        }
+        s_rowp[prt * 128 + row] = rsum;
         mma_sync_point();
         if (*abort_flag) break;
         if (tid == 0) issue_state(&tm_s, unit);  // over M' and dK
         __syncwarp();
-        float dxi[PW];
+        float dxi[PW];  // Delta dXi + D dy
         tmem_ldw<PW>(tl + tT + prt * PW, dxi);
+        {
+            const float dt = s_dt[row], D = a.D ? a.D[h] : 0.f;
+            const int c = prt * PW;
+#pragma unroll
+            for (int i = 0; i < PW / 8; ++i) {
+                float y[8];
+                if (a.D) ld8s(sm + L::oY + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), y);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) dxi[8 * i + k] = a.D ? fmaf(dt, dxi[8 * i + k], D * y[k]) : dt * dxi[8 * i + k];
+            }
+        }
         tc_before_sync();
         __syncthreads();
         // ---- T = dY S_in ----
@@ -512,10 +531,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         mma_sync_point();
         if (*abort_flag) break;
-        if (tid == 0) issue_state(&tm_g, unit);
+        if (tid == 0) {
+            issue_state(&tm_g, unit);
+            if (hh + 1 < nh) issue_y(h + 1);
+        }
         __syncwarp();
         {
-            const float e = s_e[row];
+            const float e = s_g[SsmGate::e + row];
             const int c = prt * NW;
             float dot = 0.f, t[NW], acc[NW];
             tmem_ldw<NW>(tl + tT + c, t);
@@ -564,7 +586,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         if (tid == 0 && hh + 1 < nh) issue_x(h + 1);
         __syncwarp();
         {
-            const float el = s_el[row], w = el * s_dt[row];
+            const float el = s_g[SsmGate::el + row], w = el * s_dt[row];
             const int c = prt * NW;
             float dot = 0.f, t[NW], acc[NW];
             tmem_ldw<NW>(tl + tT + c, t);
@@ -609,23 +631,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         mma_sync_point();
         if (*abort_flag) break;
-        // ---- dx over dY, and the end of the token sums ----
+        // ---- dx (a thread's columns of its row), and the end of the token sums ----
         {
-            const float el = s_el[row], dt = s_dt[row], D = a.D ? a.D[h] : 0.f;
+            const float w = s_g[SsmGate::el + row] * s_dt[row];
             const int c = prt * PW;
             float t[PW];
             tmem_ldw<PW>(tl + tT + c, t);
+            if (row < valid) {
+                uint8_t *dst = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(a.dx) +
+                                                           (((size_t)b * a.T + t0 + row) * a.H + h) * P + c);
 #pragma unroll
-            for (int i = 0; i < PW / 8; ++i) {
-                uint8_t *p = sm + L::oY + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i);
-                float y[8];
-                ld8s(p, y);
+                for (int i = 0; i < PW / 8; ++i) {
+                    float v[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float v = dt * fmaf(el, t[8 * i + k], dxi[8 * i + k]);
-                    y[k] = a.D ? fmaf(D, y[k], v) : v;
+                    for (int k = 0; k < 8; ++k) v[k] = fmaf(w, t[8 * i + k], dxi[8 * i + k]);
+                    st_bf16x8(dst + 16 * i, v);
                 }
-                st_bf16x8(p, y);
             }
         }
         if (tid < 128) {
@@ -635,12 +656,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 if (w < warp) before += s_tw[w];
                 if (w >= warp) after += s_tw[4 + w];
             }
-            const double Ah = (double)a.A[h], dlog = before + after + cross * exp2(c_last);
-            double raw = own + Ah * dlog, sA = 0.0, sD = 0.0;
-            if (a.softplus) raw *= 1.0 / (1.0 + exp(-(double)z));
+            const double dlog = before + after + cross * (double)s_g[SsmGate::elast];
+            double raw = (own + (double)a.A[h] * dlog) * (double)s_g[SsmGate::sig + tid], sA = 0.0, sD = 0.0;
             if (tid < valid) {
                 a.ddelta[((size_t)b * a.T + t0 + tid) * a.H + h] = (float)raw;
-                sA = (double)dt_own * dlog;
+                sA = (double)s_dt[tid] * dlog;
                 sD = (double)s_wd[tid];
             } else {
                 raw = 0.0;
@@ -654,26 +674,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 s_tot[warp * 3 + 2] = sD;
             }
         }
-        fence_async_smem();
         tc_before_sync();
         __syncthreads();
         if (tid < 3) part[tid * units + unit] = (float)(s_tot[tid] + s_tot[3 + tid] + s_tot[6 + tid] + s_tot[9 + tid]);
-        if (tid == 0) {
-            for (int i = 0; i < P / 64; ++i) tma_store_4d(&tm_dx, sm + L::oY + i * kTile, i * 64, h, t0, b);
-            bulk_commit();
-            bulk_wait_read_all();
-            if (hh + 1 < nh) issue_y(h + 1);
-        }
     }
     if (*abort_flag) {
         if (tid == 0) {
             record_status(GDR_ERR_TIMEOUT);
             if (bc_open) mbar_wait(bar_bc, 0);
-            if (d_x < n_x) mbar_wait(bar_x, (uint32_t)(d_x & 1));
-            if (d_y < n_y) mbar_wait(bar_y, (uint32_t)(d_y & 1));
+            mbar_wait(bar_x, (uint32_t)((n_x - 1) & 1));
+            mbar_wait(bar_y, (uint32_t)((n_y - 1) & 1));
+            mbar_wait(bar_g, (uint32_t)((n_g - 1) & 1));
             if (n_s > 0) mbar_wait(bar_s, (uint32_t)((n_s - 1) & 1));
             if (mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
-            bulk_wait_all();
         }
     } else {
         tc_after_sync();
@@ -695,7 +708,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 for (int i = 0; i < NW / 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
         }
-        if (tid == 0) bulk_wait_all();
     }
     tc_before_sync();
     __syncthreads();
@@ -742,7 +754,7 @@ inline int ssm_walk_chunks(int B, int T, int H, int P) {
 }
 
 struct SsmTcBwdWs {
-    size_t st, g, segS, segG, dec, part, dBp, dCp, total;
+    size_t gates, st, g, segS, segG, dec, part, dBp, dCp, total;
     int splits, m, R;
 };
 inline SsmTcBwdWs ssm_tc_bwd_ws(int B, int T, int H, int G, int P, int N) {
@@ -753,9 +765,10 @@ inline SsmTcBwdWs ssm_tc_bwd_ws(int B, int T, int H, int G, int P, int N) {
     w.m = ssm_walk_chunks(B, T, H, P);
     w.R = (nch + w.m - 1) / w.m;
     const size_t segs = w.R > 1 ? (size_t)B * w.R * H : 0;
-    w.st = 0;
-    w.g = ssm_align(units * P * N * 4);
-    w.segS = 2 * w.g;
+    w.gates = 0;
+    w.st = ssm_gate_bytes(B, T, H);
+    w.g = w.st + ssm_align(units * P * N * 4);
+    w.segS = w.g + ssm_align(units * P * N * 4);
     w.segG = w.segS + ssm_align(segs * P * N * 4);
     w.dec = w.segG + ssm_align(segs * P * N * 4);
     w.part = w.dec + ssm_align(segs * 4);
@@ -776,31 +789,32 @@ cudaError_t ssm_tc_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     float *dec = reinterpret_cast<float *>(base + w.dec), *part = reinterpret_cast<float *>(base + w.part);
     float *dBp = reinterpret_cast<float *>(base + w.dBp), *dCp = reinterpret_cast<float *>(base + w.dCp);
     const size_t units = (size_t)a.B * nch * a.H;
-    CUtensorMap mx, mb, mc, my, mdx, ms, mg;
+    float *gates = reinterpret_cast<float *>(base + w.gates);
+    CUtensorMap mx, mb, mc, my, ms, mg;
     if (!ssm_token_map(&mx, a.x, a.B, a.T, a.H, P, a.ldx) || !ssm_token_map(&mb, a.Bm, a.B, a.T, a.G, N, a.ldb) ||
         !ssm_token_map(&mc, a.Cm, a.B, a.T, a.G, N, a.ldc) || !ssm_token_map(&my, a.dy, a.B, a.T, a.H, P, a.H * P) ||
-        !ssm_token_map(&mdx, a.dx, a.B, a.T, a.H, P, a.H * P) || !ssm_state_map(&ms, st, units, P, N) ||
-        !ssm_state_map(&mg, g, units, P, N))
+        !ssm_state_map(&ms, st, units, P, N) || !ssm_state_map(&mg, g, units, P, N))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaSuccess;
-    if (w.R > 1) {
+    cudaError_t e = ssm_launch_gates(a, gates, s);
+    if (e == cudaSuccess && w.R > 1) {
         const dim3 grid((unsigned)(a.B * a.H) * (unsigned)w.R);
         e = ssm_launch(ssm_tc_state_kernel<P, N, false>, grid, 256, (size_t)SsmStateTc<P, N, false>::kAlloc, s, mx, mb, a, w.m,
-                       segS, dec);
+                       (const float *)gates, segS, dec);
         if (e == cudaSuccess)
             e = ssm_launch(ssm_tc_state_kernel<P, N, true>, grid, 256, (size_t)SsmStateTc<P, N, true>::kAlloc, s, my, mc, a,
-                           w.m, segG, dec);
+                           w.m, (const float *)gates, segG, dec);
         if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, w.R, a.H, P * N, segS, dec, a.S0, nullptr, s);
         if (e == cudaSuccess) e = ssm_launch_scan(true, a.B, w.R, a.H, P * N, segG, dec, a.dS_T, nullptr, s);
     }
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_walk_kernel<P, N>, dim3(2u * (P / 64) * (unsigned)(a.B * a.H) * (unsigned)w.R), 256,
-                       (size_t)SsmWalkTc<N>::kAlloc, s, mx, mb, my, mc, a, w.m, (const float *)segS, (const float *)segG, st, g);
+                       (size_t)SsmWalkTc<N>::kAlloc, s, mx, mb, my, mc, a, w.m, (const float *)gates,
+                       (const float *)segS, (const float *)segG, st, g);
     const int per = (a.H / a.G + w.splits - 1) / w.splits;
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_grad_kernel<P, N>, dim3((unsigned)((size_t)a.B * nch * a.G * w.splits)), kGradThreads,
-                       (size_t)SsmGradTc<P, N>::kAlloc, s, mx, mb, mc, my, mdx, ms, mg, a, w.splits, per,
-                       (const __nv_bfloat16 *)st, (const __nv_bfloat16 *)g, dBp, dCp, part);
+                       (size_t)SsmGradTc<P, N>::kAlloc, s, mx, mb, mc, my, ms, mg, a, w.splits, per,
+                       (const float *)gates, (const __nv_bfloat16 *)st, (const __nv_bfloat16 *)g, dBp, dCp, part);
     if (e != cudaSuccess) return e;
     if (w.splits > 1) {
         const long long total4 = (long long)a.B * a.T * a.G * (N / 4);

@@ -18,12 +18,13 @@
 // decaying state, so a product underflows only where the decay does); only the
 // four diagonal blocks take an exponential per pair.
 //
+//   0. ssm_gate_kernel      the decays of every chunk and head as tables
 // A long sequence over few heads is cut into segments of whole chunks:
 //   1. ssm_tc_state_kernel  sum_j w_j x_j B_j^T of a segment (one product over
 //      its tokens: the weights reach to the segment's end)
 //   2. ssm_scan_kernel      the states between the segments, elementwise, fp32
 //   3. ssm_tc_y_kernel      walks its segment from that state
-// One segment alone is a single launch (3 with the state written at its end).
+// One segment alone is 0 and 3, with the state written at its end.
 #pragma once
 #include <cuda.h>
 
@@ -87,12 +88,56 @@ __device__ __forceinline__ void st_split8(uint8_t *hi, uint8_t *lo, float *v) {
     sm100::st_bf16x8(lo, r);
 }
 
-// One warp: Delta and c (log2 units, 64 bits) of 128 tokens from t0.
-__device__ __forceinline__ void ssm_tc_gates(const SsmArgs &a, int b, int h, int t0, float *s_dt, double *s_c) {
-    ssm_gates<kTcQ>(a, b, h, t0, s_dt, s_c);
-    const int lane = threadIdx.x & 31;
+// ---- 0. gates ---------------------------------------------------------------------------
+// One table per unit = (b, chunk, head), read by the other kernels as one bulk copy: computed in place by a warp of
+// each of them, the softplus and the 64-bit sums took 4600 of a chunk's 9100 cycles.  Floats at:
+struct SsmGate {
+    static constexpr int dt = 0, e = 128, rowf = 256, el = 384, hi = 512, lo = 640;  // per token, see below
+    static constexpr int col = 768;                       // [I-1][96]: 2^{r_I - c_j} of the blocks I = 1..3, j < 32 I
+    static constexpr int last = 1056, elast = 1058;       // c_last (a double) and 2^{c_last}
+    static constexpr int sig = 1072, stride = 1200;       // d softplus / dz
+    static constexpr uint32_t kFwdBytes = sig * 4, kBytes = stride * 4;
+};
+// With c the sums in log2 units: e = 2^c, rowf = 2^{c - r} (r: c at the end of the block of 32 before the token's), el =
+// 2^{c_last - c}, and c in two parts (differences of nearby tokens are then exact to fp32 however far the sum has run).
+__global__ void __launch_bounds__(128) ssm_gate_kernel(SsmArgs a, float *__restrict__ gates) {
+    __shared__ double s_w[4];
+    const int nch = (a.T + kTcQ - 1) / kTcQ, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int h = blockIdx.x % a.H, bc = blockIdx.x / a.H, ch = bc % nch, b = bc / nch, tok = ch * kTcQ + t;
+    float *out = gates + (size_t)blockIdx.x * SsmGate::stride;
+    float z = 0.f, d = 0.f;
+    if (tok < a.T) {
+        z = a.delta[((size_t)b * a.T + tok) * a.H + h];
+        if (a.bias) z += a.bias[h];
+        d = a.softplus ? ssm_softplus(z) : z;
+    }
+    double c_in = (double)a.A[h] * (double)d * 1.4426950408889634074;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s_c[lane * 4 + e] *= 1.4426950408889634074;
+    for (int off = 1; off < 32; off <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, c_in, off);
+        if (lane >= off) c_in += o;
+    }
+    if (lane == 31) s_w[warp] = c_in;
+    __syncthreads();
+    double r = 0.0;
+    for (int w = 0; w < warp; ++w) r += s_w[w];
+    const double c = r + c_in, last = s_w[0] + s_w[1] + s_w[2] + s_w[3];
+    const float hi = (float)c;
+    out[SsmGate::dt + t] = d;
+    out[SsmGate::e + t] = exp2f(hi);
+    out[SsmGate::rowf + t] = exp2f((float)c_in);
+    out[SsmGate::el + t] = exp2f((float)(last - c));
+    out[SsmGate::hi + t] = hi;
+    out[SsmGate::lo + t] = (float)(c - (double)hi);
+    out[SsmGate::sig + t] = a.softplus ? 1.f / (1.f + expf(-z)) : 1.f;
+    for (int I = warp + 1; I < 4; ++I) {
+        r += s_w[I - 1];
+        out[SsmGate::col + (I - 1) * 96 + t] = exp2f((float)(r - c));
+    }
+    if (t == 0) {
+        *reinterpret_cast<double *>(out + SsmGate::last) = last;
+        out[SsmGate::elast] = exp2f((float)last);
+    }
 }
 
 // ---- 1. segment states ------------------------------------------------------------------
@@ -102,22 +147,23 @@ struct SsmStateTc {
     static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile;
     static constexpr uint32_t oX = 0, oB = XB, oHi = oB + BB, oLo = oHi + BB, oZero = oLo + BB;
     static constexpr uint32_t kHiBlock = N == 64 ? 2 * kTile : kTile;  // distance of the second 64 lanes
-    static constexpr uint32_t oCtl = oZero + (N == 64 ? kTile : 0);
-    static constexpr uint32_t kAlloc = oCtl + 128 * 4 + 128 * 8 + 128 + 1024;
+    static constexpr uint32_t oGate = oZero + (N == 64 ? kTile : 0);
+    static constexpr uint32_t oCtl = oGate + SsmGate::kFwdBytes;
+    static constexpr uint32_t kAlloc = oCtl + 64 + 1024;
 };
 
 template <int P, int N, bool BWD>
 __global__ void __launch_bounds__(256) ssm_tc_state_kernel(const __grid_constant__ CUtensorMap tm_x,
                                                            const __grid_constant__ CUtensorMap tm_b, SsmArgs a, int m,
-                                                           float *__restrict__ out, float *__restrict__ dec) {
+                                                           const float *__restrict__ gates, float *__restrict__ out,
+                                                           float *__restrict__ dec) {
     using L = SsmStateTc<P, N, BWD>;
     using namespace sm100;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
-    double *s_c = reinterpret_cast<double *>(sm + L::oCtl);
-    float *s_dt = reinterpret_cast<float *>(s_c + 128);
-    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(s_dt + 128), *mma_bar = tma_bar + 1;
+    const float *s_g = reinterpret_cast<const float *>(sm + L::oGate);
+    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(sm + L::oCtl), *mma_bar = tma_bar + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tma_bar + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -143,7 +189,9 @@ __global__ void __launch_bounds__(256) ssm_tc_state_kernel(const __grid_constant
     // forward: chunks from the last, so that the decay to the segment's end is known; backward: from the first
     auto chunk = [&](int k) { return BWD ? c0 + k : c0 + cn - 1 - k; };
     auto issue = [&](int k) {
-        mbar_expect_tx(tma_bar, L::XB + L::BB);
+        mbar_expect_tx(tma_bar, L::XB + L::BB + SsmGate::kFwdBytes);
+        bulk_load_g2s(sm + L::oGate, gates + (((size_t)b * nch + chunk(k)) * a.H + h) * SsmGate::stride, SsmGate::kFwdBytes,
+                      tma_bar);
         for (int i = 0; i < P / 64; ++i) tma_load_4d(sm + L::oX + i * kTile, &tm_x, tma_bar, i * 64, h, chunk(k) * kTcQ, b);
         for (int i = 0; i < N / 64; ++i) tma_load_4d(sm + L::oB + i * kTile, &tm_b, tma_bar, i * 64, g, chunk(k) * kTcQ, b);
     };
@@ -153,15 +201,14 @@ __global__ void __launch_bounds__(256) ssm_tc_state_kernel(const __grid_constant
     int k = 0;
 #pragma unroll 1
     for (; k < cn; ++k) {
-        if (warp == 1) ssm_tc_gates(a, b, h, chunk(k) * kTcQ, s_dt, s_c);
         if (tid == 0 && !mbar_wait(tma_bar, (uint32_t)(k & 1))) *abort_flag = 1;
         __syncthreads();
         if (*abort_flag) break;
         {   // the weighted rows in two bf16 parts: row tid & 127, half of the columns
             const int r = tid & 127, half = tid >> 7;
-            const double last = s_c[127];
-            const float w = BWD ? exp2f((float)(s_c[r] + edge)) : s_dt[r] * exp2f((float)(last - s_c[r] + edge));
-            edge += last;
+            const float far = exp2f((float)edge);
+            const float w = BWD ? s_g[SsmGate::e + r] * far : s_g[SsmGate::dt + r] * s_g[SsmGate::el + r] * far;
+            edge += *reinterpret_cast<const double *>(s_g + SsmGate::last);
             constexpr int CH = N / 16;  // 16-byte chunks of a half row
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -225,67 +272,38 @@ __global__ void __launch_bounds__(256) ssm_tc_state_kernel(const __grid_constant
 }
 
 // ---- 3. outputs ------------------------------------------------------------------------------
-// LO: the state's own product takes both parts of w B, and S_T is written at the end (one segment).
+// LO: the state's own product takes both parts of w B, and S_T is written at the end (one segment).  With P = 64 two
+// CTAs of 8 warps share an SM; with P = 128 (the shared memory of one) a CTA has 16.
 template <int P, int N, bool LO>
 struct SsmYTc {
+    static constexpr int NT = P == 128 ? 512 : 256, kParts = NT / 128;  // warps of one TMEM quarter: column parts
     static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile;
     static constexpr uint32_t oX = 0, oB = XB, oLo = oB + BB, oZero = oLo + (LO ? BB : 0);
     static constexpr uint32_t kHiBlock = N == 64 ? (LO ? 2 : 1) * kTile : kTile;
     static constexpr uint32_t oC = oZero + (N == 64 ? kTile : 0);  // C, then the decayed scores
     static constexpr uint32_t kSBlock = N * 128;                   // S^T: N rows of 64 columns p
     static constexpr uint32_t oS = oC + 2 * kTile;
-    static constexpr uint32_t oGate = oS + P / 64 * kSBlock;
-    // doubles c[2][128]; floats dt[2][128], e[128], row[128], w[128], col[3][96], hi[128], lo[128]
-    static constexpr uint32_t kGate = 2 * 128 * 8 + (2 * 128 + 3 * 128 + 3 * 96 + 2 * 128) * 4;
-    static constexpr uint32_t oBar = oGate + kGate;
+    static constexpr uint32_t oGate = oS + P / 64 * kSBlock;       // two tables
+    static constexpr uint32_t oBar = oGate + 2 * SsmGate::kFwdBytes;
     static constexpr uint32_t kAlloc = oBar + 64 + 1024;
     static constexpr uint32_t kTmemCols = P == 64 ? 256 : 512;
 };
 
-// The tables of one chunk from its Delta and c (log2): e_i = 2^{c_i}, row factor 2^{c_i - r} (r: c at the end of
-// the block of 32 before i's), w_j, column factors Delta_j 2^{r_I - c_j} of the blocks I = 1..3, and c in two parts
-// (differences of nearby tokens are then exact to fp32 however far the sum has run).
-__device__ __forceinline__ void ssm_tc_tables(const float *s_dt, const double *s_c, float *s_e, float *s_row, float *s_w,
-                                              float *s_col, float *s_hi, float *s_lo) {
-    const int tid = threadIdx.x;
-    const double last = s_c[127];
-    if (tid < 128) {
-        const double c = s_c[tid];
-        const double r = tid >= 32 ? s_c[(tid & ~31) - 1] : 0.0;
-        s_e[tid] = exp2f((float)c);
-        s_row[tid] = exp2f((float)(c - r));
-        s_w[tid] = s_dt[tid] * exp2f((float)(last - c));
-        const float hi = (float)c;
-        s_hi[tid] = hi;
-        s_lo[tid] = (float)(c - (double)hi);
-    } else {
-        for (int i = tid - 128; i < 192; i += 128) {  // 32 + 64 + 96 pairs (I, j < 32 I)
-            const int I = i < 32 ? 1 : i < 96 ? 2 : 3, j = i < 32 ? i : i < 96 ? i - 32 : i - 96;
-            s_col[(I - 1) * 96 + j] = s_dt[j] * exp2f((float)(s_c[32 * I - 1] - s_c[j]));
-        }
-    }
-}
-
 template <int P, int N, bool LO>
-__global__ void __launch_bounds__(256, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(const __grid_constant__ CUtensorMap tm_x,
-                                                       const __grid_constant__ CUtensorMap tm_b,
-                                                       const __grid_constant__ CUtensorMap tm_c,
-                                                       const __grid_constant__ CUtensorMap tm_y, SsmArgs a, int m,
-                                                       const float *__restrict__ states) {
+__global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(
+    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
+    const __grid_constant__ CUtensorMap tm_c, SsmArgs a, int m, const float *__restrict__ gates,
+    const float *__restrict__ states) {
     using L = SsmYTc<P, N, LO>;
     using namespace sm100;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
-    double *s_c2 = reinterpret_cast<double *>(sm + L::oGate);
-    float *s_dt2 = reinterpret_cast<float *>(s_c2 + 256);
-    float *s_e = s_dt2 + 256, *s_row = s_e + 128, *s_w = s_row + 128, *s_col = s_w + 128, *s_hi = s_col + 288,
-          *s_lo = s_hi + 128;
-    uint64_t *bar_x = reinterpret_cast<uint64_t *>(sm + L::oBar), *bar_bc = bar_x + 1, *mma_bar = bar_x + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_x + 3);
+    uint64_t *bar_x = reinterpret_cast<uint64_t *>(sm + L::oBar), *bar_bc = bar_x + 1, *bar_g = bar_x + 2, *mma_bar = bar_x + 3;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_x + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;  // TMEM lane (token i or state row n), column half
+    const int q = warp & 3, prt = warp >> 2, row = q * 32 + lane;  // TMEM lane (token i or state row n), column part
     const int nch = (a.T + kTcQ - 1) / kTcQ, R = (nch + m - 1) / m;
     const int seg = blockIdx.x % R, bh = blockIdx.x / R, h = bh % a.H, b = bh / a.H, g = h / (a.H / a.G);
     const int c0 = seg * m, cn = min(m, nch - c0);
@@ -293,19 +311,21 @@ __global__ void __launch_bounds__(256, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(c
     if (tid == 0) {
         mbar_init(bar_x, 1);
         mbar_init(bar_bc, 1);
+        mbar_init(bar_g, 1);
         mbar_init(mma_bar, 1);
         fence_mbar_init();
         *abort_flag = 0;
     }
     if (warp == 0) tmem_alloc(tmem_slot, L::kTmemCols);
     if (N == 64)
-        for (int i = tid; i < (int)kTile / 16; i += 256) reinterpret_cast<uint4 *>(sm + L::oZero)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < (int)kTile / 16; i += L::NT) reinterpret_cast<uint4 *>(sm + L::oZero)[i] = make_uint4(0, 0, 0, 0);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     constexpr uint32_t tK = 0, tY2 = 128, tS = 128 + P;  // Y1 takes K's columns once K is read
+    const int cp = prt * 32;                             // this warp's 32 columns p
 
     auto issue_bc = [&](int k) {
         mbar_expect_tx(bar_bc, 2 * L::BB);
@@ -318,22 +338,24 @@ __global__ void __launch_bounds__(256, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(c
         mbar_expect_tx(bar_x, L::XB);
         for (int i = 0; i < P / 64; ++i) tma_load_4d(sm + L::oX + i * kTile, &tm_x, bar_x, i * 64, h, (c0 + k) * kTcQ, b);
     };
-    int n_bc = 0, n_x = 0, d_bc = 0, d_x = 0;  // issued and awaited, by thread 0
+    auto issue_g = [&](int k) {
+        mbar_expect_tx(bar_g, SsmGate::kFwdBytes);
+        bulk_load_g2s(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes,
+                      gates + (((size_t)b * nch + c0 + k) * a.H + h) * SsmGate::stride, SsmGate::kFwdBytes, bar_g);
+    };
+    int n_bc = 0, n_x = 0, n_g = 0;  // issued, by thread 0
     if (tid == 0) {
+        issue_g(0);
         issue_bc(0);
         issue_x(0);
-        n_bc = n_x = 1;
+        n_bc = n_x = n_g = 1;
     }
-    if (warp == 1) ssm_tc_gates(a, b, h, c0 * kTcQ, s_dt2, s_c2);
     {   // the entering state: lane n, columns p
         const float *src = states ? states + (((size_t)b * R + seg) * a.H + h) * P * N : a.S0 ? a.S0 + (size_t)bh * P * N : nullptr;
-#pragma unroll 1
-        for (int c = half * (P / 2); c < (half + 1) * (P / 2); c += 32) {
-            float v[32];
+        float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = src && row < N ? src[(size_t)(c + i) * N + row] : 0.f;
-            tmem_st32(tl + tS + c, v);
-        }
+        for (int i = 0; i < 32; ++i) v[i] = src && row < N ? src[(size_t)(cp + i) * N + row] : 0.f;
+        tmem_st32(tl + tS + cp, v);
         tmem_wait_st();
     }
     uint32_t mma_phase = 0;
@@ -349,32 +371,33 @@ __global__ void __launch_bounds__(256, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(c
         tc_after_sync();
     };
     const float D = a.D ? a.D[h] : 0.f;
-    __syncthreads();
 
 #pragma unroll 1
     for (int k = 0; k < cn; ++k) {
-        const double *s_c = s_c2 + (k & 1) * 128;
-        const float *s_dt = s_dt2 + (k & 1) * 128;
-        ssm_tc_tables(s_dt, s_c, s_e, s_row, s_w, s_col, s_hi, s_lo);
+        const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes);
+        if (tid == 0) {
+            if (!mbar_wait(bar_g, (uint32_t)(k & 1))) *abort_flag = 1;
+        }
+        __syncthreads();
+        if (*abort_flag) break;
+        if (tid == 0 && k + 1 < cn) {  // the other table was last read a chunk ago
+            issue_g(k + 1);
+            ++n_g;
+        }
+        __syncwarp();
         if (row < N) {  // S^T as the bf16 operand [n][p]; the fp32 state decays to the chunk's end
-            const float el = exp2f((float)s_c[127]);
-#pragma unroll 1
-            for (int c = half * (P / 2); c < (half + 1) * (P / 2); c += 32) {
-                float v[32];
-                tmem_ld32(tl + tS + c, v);
+            const float el = s_g[SsmGate::elast];
+            float v[32];
+            tmem_ld32(tl + tS + cp, v);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    st_bf16x8(sm + L::oS + (c >> 6) * L::kSBlock + sw128_offset(row, ((c & 63) >> 3) + i), v + 8 * i);
+            for (int i = 0; i < 4; ++i)
+                st_bf16x8(sm + L::oS + (cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i), v + 8 * i);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= el;
-                tmem_st32(tl + tS + c, v);
-            }
+            for (int i = 0; i < 32; ++i) v[i] *= el;
+            tmem_st32(tl + tS + cp, v);
             tmem_wait_st();
         }
-        if (tid == 0) {
-            if (!mbar_wait(bar_bc, (uint32_t)(k & 1))) *abort_flag = 1;
-            else ++d_bc;
-        }
+        if (tid == 0 && !mbar_wait(bar_bc, (uint32_t)(k & 1))) *abort_flag = 1;
         fence_async_smem();
         tc_before_sync();
         __syncthreads();
@@ -389,43 +412,52 @@ __global__ void __launch_bounds__(256, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(c
                 mma_bf16(tmem + tY2, desc_k(sb + L::oC, kk), desc_mn(sb + L::oS, kk, L::kSBlock),
                          idesc_bf16(128, P, false, true), kk > 0);
         }
-        if (warp == 1 && k + 1 < cn)
-            ssm_tc_gates(a, b, h, (c0 + k + 1) * kTcQ, s_dt2 + ((k + 1) & 1) * 128, s_c2 + ((k + 1) & 1) * 128);
         mma_sync_point();
         if (*abort_flag) break;
 
         // decayed scores -> bf16 [i][j] over C (C's products are done)
-        const float rf = s_row[row], ci = s_hi[row], cl = s_lo[row];
+        const float rf = s_g[SsmGate::rowf + row], ci = s_g[SsmGate::hi + row], cl = s_g[SsmGate::lo + row];
 #pragma unroll
-        for (int jb = 0; jb < 2; ++jb) {
-            const int J = half * 2 + jb;  // 32-column block
-            uint8_t *dst = sm + L::oC + half * kTile;
+        for (int jb = 0; jb < 4 / L::kParts; ++jb) {
+            const int J = prt * (4 / L::kParts) + jb;  // 32-column block
+            uint8_t *dst = sm + L::oC + (J >> 1) * kTile;
             float v[32];
             if (J > q) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0.f;
             } else {
+                const float4 *dt4 = reinterpret_cast<const float4 *>(s_g + SsmGate::dt + J * 32);
                 tmem_ld32(tl + tK + J * 32, v);
                 if (J < q) {
-                    const float *col = s_col + (q - 1) * 96 + J * 32;
+                    const float4 *col4 = reinterpret_cast<const float4 *>(s_g + SsmGate::col + (q - 1) * 96 + J * 32);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= rf * col[i];
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 cc = col4[i], d = dt4[i];
+                        v[4 * i] *= rf * cc.x * d.x;
+                        v[4 * i + 1] *= rf * cc.y * d.y;
+                        v[4 * i + 2] *= rf * cc.z * d.z;
+                        v[4 * i + 3] *= rf * cc.w * d.w;
+                    }
                 } else {
+                    const float4 *hi4 = reinterpret_cast<const float4 *>(s_g + SsmGate::hi + J * 32);
+                    const float4 *lo4 = reinterpret_cast<const float4 *>(s_g + SsmGate::lo + J * 32);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int j = J * 32 + i;
-                        const float e = exp2f((ci - s_hi[j]) + (cl - s_lo[j])) * s_dt[j];
-                        v[i] = i <= lane ? v[i] * e : 0.f;
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 hj = hi4[i], lj = lo4[i], d = dt4[i];
+                        const float e[4] = {ex2_ftz((ci - hj.x) + (cl - lj.x)) * d.x, ex2_ftz((ci - hj.y) + (cl - lj.y)) * d.y,
+                                            ex2_ftz((ci - hj.z) + (cl - lj.z)) * d.z, ex2_ftz((ci - hj.w) + (cl - lj.w)) * d.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) v[4 * i + u] = 4 * i + u <= lane ? v[4 * i + u] * e[u] : 0.f;
                     }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st_bf16x8(dst + sw128_offset(row, jb * 4 + i), v + 8 * i);
+            for (int i = 0; i < 4; ++i) st_bf16x8(dst + sw128_offset(row, (J & 1) * 4 + i), v + 8 * i);
         }
         if (LO || k + 1 < cn) {  // w B in place (B's product is done), its second part beside it
             const int r = tid & 127;
-            const float w = s_w[r];
-            constexpr int CH = N / 16;
+            const float w = s_g[SsmGate::dt + r] * s_g[SsmGate::el + r];
+            constexpr int CH = N / 8 / L::kParts;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int c = (tid >> 7) * CH + i;
@@ -438,10 +470,7 @@ __global__ void __launch_bounds__(256, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(c
                 else st_bf16x8(p, v);
             }
         }
-        if (tid == 0) {
-            if (!mbar_wait(bar_x, (uint32_t)(k & 1))) *abort_flag = 1;
-            else ++d_x;
-        }
+        if (tid == 0 && !mbar_wait(bar_x, (uint32_t)(k & 1))) *abort_flag = 1;
         fence_async_smem();
         tc_before_sync();
         __syncthreads();
@@ -460,66 +489,56 @@ __global__ void __launch_bounds__(256, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(c
                                  desc_mn(sb + L::oX, kk), idesc_bf16(128, P, true, true), 1);
             }
         }
+        uint4 xr[4];  // this thread's x, before its tile is filled again
+        if (a.D)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                xr[i] = *reinterpret_cast<const uint4 *>(sm + L::oX + (uint32_t)(cp >> 6) * kTile +
+                                                         sw128_offset(row, ((cp & 63) >> 3) + i));
         mma_sync_point();
         if (*abort_flag) break;
         if (tid == 0 && k + 1 < cn) {
             issue_bc(k + 1);
+            issue_x(k + 1);
             ++n_bc;
+            ++n_x;
         }
-        {   // y = Y1 + e^{c_i} Y2 + D x over the x tile
-            const float e = s_e[row];
-#pragma unroll 1
-            for (int c = half * (P / 2); c < (half + 1) * (P / 2); c += 32) {
-                float y1[32], y2[32];
-                tmem_ld32(tl + tK + c, y1);
-                tmem_ld32(tl + tY2 + c, y2);
+        __syncwarp();
+        {   // y = Y1 + e^{c_i} Y2 + D x: 64 bytes of a row a thread
+            const float e = s_g[SsmGate::e + row];
+            const int t = (c0 + k) * kTcQ + row;
+            float y1[32], y2[32];
+            tmem_ld32(tl + tK + cp, y1);
+            tmem_ld32(tl + tY2 + cp, y2);
+            uint8_t *dst = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(a.y) + (((size_t)b * a.T + t) * a.H + h) * P + cp);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint8_t *p = sm + L::oX + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i);
-                    float x[8];
-                    ld8s(p, x);
+            for (int i = 0; i < 4; ++i) {
+                float x[8];
+                if (a.D) ld8s(reinterpret_cast<const uint8_t *>(&xr[i]), x);
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const float y = fmaf(e, y2[8 * i + u], y1[8 * i + u]);
-                        x[u] = a.D ? fmaf(D, x[u], y) : y;
-                    }
-                    st_bf16x8(p, x);
+                for (int u = 0; u < 8; ++u) {
+                    const float y = fmaf(e, y2[8 * i + u], y1[8 * i + u]);
+                    x[u] = a.D ? fmaf(D, x[u], y) : y;
                 }
+                if (t < a.T) st_bf16x8(dst + 16 * i, x);
             }
         }
-        fence_async_smem();
         tc_before_sync();
-        __syncthreads();
-        if (tid == 0) {
-            for (int i = 0; i < P / 64; ++i) tma_store_4d(&tm_y, sm + L::oX + i * kTile, i * 64, h, (c0 + k) * kTcQ, b);
-            bulk_commit();
-            bulk_wait_read_all();
-            if (k + 1 < cn) {
-                issue_x(k + 1);
-                ++n_x;
-            }
-        }
     }
     if (*abort_flag) {
-        if (tid == 0) {  // wait, bounded, for what is still in flight
+        if (tid == 0) {  // wait, bounded, for the last of each copy and for the products
             record_status(GDR_ERR_TIMEOUT);
-            if (d_bc < n_bc) mbar_wait(bar_bc, (uint32_t)(d_bc & 1));
-            if (d_x < n_x) mbar_wait(bar_x, (uint32_t)(d_x & 1));
+            mbar_wait(bar_g, (uint32_t)((n_g - 1) & 1));
+            mbar_wait(bar_bc, (uint32_t)((n_bc - 1) & 1));
+            mbar_wait(bar_x, (uint32_t)((n_x - 1) & 1));
             if (mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
-            bulk_wait_all();
         }
-    } else {
-        if (LO && a.S_T && row < N) {
-            float *dst = a.S_T + (size_t)bh * P * N;
-#pragma unroll 1
-            for (int c = half * (P / 2); c < (half + 1) * (P / 2); c += 32) {
-                float v[32];
-                tmem_ld32(tl + tS + c, v);
+    } else if (LO && a.S_T && row < N) {
+        float *dst = a.S_T + (size_t)bh * P * N;
+        float v[32];
+        tmem_ld32(tl + tS + cp, v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) dst[(size_t)(c + i) * N + row] = v[i];
-            }
-        }
-        if (tid == 0) bulk_wait_all();
+        for (int i = 0; i < 32; ++i) dst[(size_t)(cp + i) * N + row] = v[i];
     }
     tc_before_sync();
     __syncthreads();
@@ -562,38 +581,52 @@ inline int ssm_tc_chunks(int B, int T, int H, int P) {
 }
 
 struct SsmTcFwdWs {
-    size_t st, dec, total;
+    size_t gates, st, dec, total;
 };
+inline size_t ssm_gate_bytes(int B, int T, int H) {
+    return ssm_align((size_t)B * ((T + kTcQ - 1) / kTcQ) * H * SsmGate::kBytes);
+}
 inline SsmTcFwdWs ssm_tc_fwd_ws(int B, int T, int H, int P, int N) {
     const int m = ssm_tc_chunks(B, T, H, P), nch = (T + kTcQ - 1) / kTcQ, R = (nch + m - 1) / m;
     SsmTcFwdWs w{};
+    w.st = w.dec = w.total = ssm_gate_bytes(B, T, H);
     if (R == 1) return w;
     const size_t units = (size_t)B * R * H;
-    w.dec = ssm_align(units * P * N * 4);
+    w.dec = w.st + ssm_align(units * P * N * 4);
     w.total = w.dec + ssm_align(units * 4);
     return w;
 }
 
+inline cudaError_t ssm_launch_gates(const SsmArgs &a, float *gates, cudaStream_t s) {
+    const unsigned units = (unsigned)((size_t)a.B * ((a.T + kTcQ - 1) / kTcQ) * a.H);
+    ssm_gate_kernel<<<units, 128, 0, s>>>(a, gates);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cudaGetLastError();
+}
+
 template <int P, int N>
 cudaError_t ssm_tc_fwd(const SsmArgs &a, void *ws, cudaStream_t s) {
-    CUtensorMap mx, mb, mc, my;
+    CUtensorMap mx, mb, mc;
     if (!ssm_token_map(&mx, a.x, a.B, a.T, a.H, P, a.ldx) || !ssm_token_map(&mb, a.Bm, a.B, a.T, a.G, N, a.ldb) ||
-        !ssm_token_map(&mc, a.Cm, a.B, a.T, a.G, N, a.ldc) || !ssm_token_map(&my, a.y, a.B, a.T, a.H, P, a.H * P))
+        !ssm_token_map(&mc, a.Cm, a.B, a.T, a.G, N, a.ldc))
         return cudaErrorInvalidValue;
     const int m = ssm_tc_chunks(a.B, a.T, a.H, P), nch = (a.T + kTcQ - 1) / kTcQ, R = (nch + m - 1) / m;
     const dim3 grid((unsigned)(a.B * a.H) * (unsigned)R);
-    if (R == 1)
-        return ssm_launch(ssm_tc_y_kernel<P, N, true>, grid, 256, (size_t)SsmYTc<P, N, true>::kAlloc, s, mx, mb, mc, my, a, m,
-                          (const float *)nullptr);
     const SsmTcFwdWs w = ssm_tc_fwd_ws(a.B, a.T, a.H, P, N);
+    float *gates = static_cast<float *>(ws);
+    cudaError_t e = ssm_launch_gates(a, gates, s);
+    if (e != cudaSuccess) return e;
+    if (R == 1)
+        return ssm_launch(ssm_tc_y_kernel<P, N, true>, grid, SsmYTc<P, N, true>::NT, (size_t)SsmYTc<P, N, true>::kAlloc, s, mx,
+                          mb, mc, a, m, (const float *)gates, (const float *)nullptr);
     float *st = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.st);
     float *dec = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.dec);
-    cudaError_t e = ssm_launch(ssm_tc_state_kernel<P, N, false>, grid, 256, (size_t)SsmStateTc<P, N, false>::kAlloc, s, mx, mb,
-                               a, m, st, dec);
+    e = ssm_launch(ssm_tc_state_kernel<P, N, false>, grid, 256, (size_t)SsmStateTc<P, N, false>::kAlloc, s, mx, mb, a, m,
+                   (const float *)gates, st, dec);
     if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, R, a.H, P * N, st, dec, a.S0, a.S_T, s);
     if (e == cudaSuccess)
-        e = ssm_launch(ssm_tc_y_kernel<P, N, false>, grid, 256, (size_t)SsmYTc<P, N, false>::kAlloc, s, mx, mb, mc, my, a, m,
-                       (const float *)st);
+        e = ssm_launch(ssm_tc_y_kernel<P, N, false>, grid, SsmYTc<P, N, false>::NT, (size_t)SsmYTc<P, N, false>::kAlloc, s, mx,
+                       mb, mc, a, m, (const float *)gates, (const float *)st);
     return e;
 }
 

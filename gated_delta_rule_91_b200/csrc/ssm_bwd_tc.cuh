@@ -2,7 +2,7 @@
 // tensor cores, bf16 inputs, P, N in {64, 128}; formulas at the gradient kernel
 // of ssm_simt.cuh.  Chunks of 128 tokens:
 //   1. ssm_tc_walk_kernel   S_in(c) of every chunk, walking forwards, and G_out(c),
-//      walking backwards, in one launch (segments from ssm_tc_state_kernel and
+//      walking backwards, in one launch (segments from the same walk and
 //      ssm_scan_kernel first where heads are few), each state as two bf16 parts
 //   2. ssm_tc_grad_kernel   a CTA owns one chunk of one group and walks heads of
 //      it, so that C B^T is formed once and dB, dC are summed over the heads in
@@ -23,188 +23,6 @@
 
 namespace gdr {
 
-// A state's two bf16 parts in memory: [unit][part][N][P], unit = (b, chunk, head).
-inline bool ssm_state_map(CUtensorMap *map, const void *base, size_t units, int P, int N) {
-    SsmEncodeFn enc = ssm_encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)P, (cuuint64_t)N, 2, (cuuint64_t)units};
-    const cuuint64_t strides[3] = {(cuuint64_t)P * 2, (cuuint64_t)N * P * 2, (cuuint64_t)2 * N * P * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)N, 1, 1}, estr[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// ---- 1. the states of every chunk --------------------------------------------------------
-// A CTA walks the chunks of one (b, h, segment) for 64 columns p of the state, forwards (S) or backwards (G); the
-// state stays in TMEM (lanes n, fp32).  Per chunk: write the state as it enters (in walking order), scale it by the
-// chunk's decay, and add (w B)^T X, or (e^c C)^T dY, with the weighted rows in two bf16 parts (the first in place).
-template <int N>
-struct SsmWalkTc {
-    static constexpr uint32_t BB = N / 64 * kTile;
-    static constexpr uint32_t oX = 0, oHi = kTile, oLo = oHi + BB, oZero = oLo + BB;
-    static constexpr uint32_t kHiBlock = N == 64 ? 2 * kTile : kTile;
-    static constexpr uint32_t oGate = oZero + (N == 64 ? kTile : 0);  // two tables
-    static constexpr uint32_t oCtl = oGate + 2 * SsmGate::kFwdBytes;
-    static constexpr uint32_t kAlloc = oCtl + 64 + 1024;
-};
-
-template <int P, int N>
-__global__ void __launch_bounds__(256, 2) ssm_tc_walk_kernel(
-    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
-    const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_c, SsmArgs a, int m,
-    const float *__restrict__ gates, const float *__restrict__ seg_S, const float *__restrict__ seg_G,
-    __nv_bfloat16 *__restrict__ out_S,
-    __nv_bfloat16 *__restrict__ out_G) {
-    using L = SsmWalkTc<N>;
-    using namespace sm100;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const uint32_t sb = smem_u32(sm);
-    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(sm + L::oCtl), *mma_bar = tma_bar + 1, *bar_g = tma_bar + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tma_bar + 3);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
-    const int nch = (a.T + kTcQ - 1) / kTcQ, R = (nch + m - 1) / m;
-    int u = blockIdx.x;
-    const bool rev = u & 1;
-    u >>= 1;
-    const int p0 = P == 128 ? (u & 1) * 64 : 0;
-    if (P == 128) u >>= 1;
-    const int seg = u % R, bh = u / R, h = bh % a.H, b = bh / a.H, g = h / (a.H / a.G);
-    const int c0 = seg * m, cn = min(m, nch - c0);
-    auto chunk = [&](int k) { return rev ? c0 + cn - 1 - k : c0 + k; };
-
-    if (tid == 0) {
-        mbar_init(tma_bar, 1);
-        mbar_init(mma_bar, 1);
-        mbar_init(bar_g, 1);
-        fence_mbar_init();
-        *abort_flag = 0;
-    }
-    if (warp == 0) tmem_alloc(tmem_slot, 64);
-    if (N == 64)
-        for (int i = tid; i < (int)kTile / 16; i += 256) reinterpret_cast<uint4 *>(sm + L::oZero)[i] = make_uint4(0, 0, 0, 0);
-    tc_before_sync();
-    __syncthreads();
-    tc_after_sync();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + half * 32;
-    auto issue = [&](int k) {
-        mbar_expect_tx(tma_bar, kTile + L::BB);
-        tma_load_4d(sm + L::oX, rev ? &tm_dy : &tm_x, tma_bar, p0, h, chunk(k) * kTcQ, b);
-        for (int i = 0; i < N / 64; ++i)
-            tma_load_4d(sm + L::oHi + i * kTile, rev ? &tm_c : &tm_b, tma_bar, i * 64, g, chunk(k) * kTcQ, b);
-    };
-    auto issue_g = [&](int k) {
-        mbar_expect_tx(bar_g, SsmGate::kFwdBytes);
-        bulk_load_g2s(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes,
-                      gates + (((size_t)b * nch + chunk(k)) * a.H + h) * SsmGate::stride, SsmGate::kFwdBytes, bar_g);
-    };
-    int n_x = 1, n_g = 1;
-    if (tid == 0) {
-        issue_g(0);
-        issue(0);
-    }
-    float v[32];
-    {
-        const float *src = R > 1 ? (rev ? seg_G : seg_S) + (((size_t)b * R + seg) * a.H + h) * P * N
-                                 : (rev ? a.dS_T : a.S0);
-        if (R == 1 && src) src += (size_t)bh * P * N;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = src && row < N ? src[(size_t)(p0 + half * 32 + i) * N + row] : 0.f;
-        tmem_st32(tl, v);
-        tmem_wait_st();
-    }
-    bool pending = false;
-    int k = 0;
-#pragma unroll 1
-    for (; k < cn; ++k) {
-        const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes);
-        if (!mbar_wait(bar_g, (uint32_t)(k & 1))) *abort_flag = 1;  // every thread
-        if (row < N) {  // the state as it enters, and its decay
-            const float el = s_g[SsmGate::elast];
-            const size_t unit = ((size_t)b * nch + chunk(k)) * a.H + h;
-            uint8_t *hi = reinterpret_cast<uint8_t *>((rev ? out_G : out_S) + ((unit * 2) * N + row) * P + p0 + half * 32);
-            uint8_t *lo = hi + (size_t)N * P * 2;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st_split8(hi + 16 * i, lo + 16 * i, v + 8 * i);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= el;
-            tmem_st32(tl, v);
-            tmem_wait_st();
-        }
-        const bool last_one = k + 1 == cn && !(rev && seg == 0 && a.dS0);  // nothing reads the state after it
-        if (tid == 0 && !mbar_wait(tma_bar, (uint32_t)(k & 1))) *abort_flag = 1;
-        __syncthreads();
-        if (*abort_flag || last_one) break;
-        if (tid == 0 && k + 1 < cn) {  // the other table was last read a chunk ago
-            issue_g(k + 1);
-            ++n_g;
-        }
-        __syncwarp();
-        {
-            const int r = tid & 127, hf = tid >> 7;
-            const float w = rev ? s_g[SsmGate::e + r] : s_g[SsmGate::dt + r] * s_g[SsmGate::el + r];
-            constexpr int CH = N / 16;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = hf * CH + i;
-                const uint32_t off = (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
-                float x[8];
-                ld8s(sm + L::oHi + off, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= w;
-                st_split8(sm + L::oHi + off, sm + L::oLo + off, x);
-            }
-        }
-        fence_async_smem();
-        tc_before_sync();
-        __syncthreads();
-        if (tid == 0) {
-            tc_after_sync();
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16(tmem, desc_mn(sb + (part ? L::oLo : L::oHi), kk, part ? kTile : L::kHiBlock),
-                             desc_mn(sb + L::oX, kk), idesc_bf16(128, 64, true, true), 1);
-            mma_commit(mma_bar);
-        }
-        if (tid == 0) {
-            if (!mbar_wait(mma_bar, (uint32_t)(k & 1))) {
-                *abort_flag = 1;
-                pending = true;
-            } else if (k + 1 < cn) {
-                issue(k + 1);
-                ++n_x;
-            }
-        }
-        __syncthreads();
-        if (*abort_flag) break;
-        tc_after_sync();
-        tmem_ld32(tl, v);
-    }
-    if (*abort_flag) {
-        if (tid == 0) {
-            record_status(GDR_ERR_TIMEOUT);
-            if (pending) mbar_wait(mma_bar, (uint32_t)(k & 1));
-            mbar_wait(tma_bar, (uint32_t)((n_x - 1) & 1));
-            mbar_wait(bar_g, (uint32_t)((n_g - 1) & 1));
-        }
-    } else if (rev && seg == 0 && a.dS0 && row < N) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) a.dS0[((size_t)bh * P + p0 + half * 32 + i) * N + row] = v[i];
-    }
-    tc_before_sync();
-    __syncthreads();
-    if (warp == 0) {
-        tc_after_sync();
-        tmem_dealloc(tmem, 64);
-    }
-}
-
 // ---- 2. the gradients of every chunk -------------------------------------------------------
 template <int P, int N>
 struct SsmGradTc {
@@ -214,10 +32,10 @@ struct SsmGradTc {
     static constexpr uint32_t oM = oR, oK = oR + 2 * kTile;   // M', dK
     static constexpr uint32_t oHi = oR, oLo = oR + SB;        // S_in, then G_out
     static constexpr uint32_t oGate = oR + 4 * kTile;
-    // two tables; doubles: warp sums of the token sums [4][2], totals [4][3], <G, S> [16]; floats rowp[4][128],
+    // two tables; doubles: warp sums of the token sums [4][2]; floats: totals [4][3], <G, S> [20], rowp[4][128],
     // colp[4][128], diag, wd, gxp[4][128], syp[4][128]
     static constexpr uint32_t oSum = oGate + 2 * SsmGate::kBytes;
-    static constexpr uint32_t oBar = oSum + (8 + 12 + 16) * 8 + 18 * 128 * 4;
+    static constexpr uint32_t oBar = oSum + 8 * 8 + (12 + 20 + 18 * 128) * 4;
     static constexpr uint32_t kAlloc = oBar + 64 + 1024;
 };
 
@@ -243,12 +61,6 @@ __device__ __forceinline__ double ssm_warp_scan(double x) {  // inclusive
     }
     return x;
 }
-__device__ __forceinline__ double ssm_warp_sum(double x) {
-#pragma unroll
-    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    return x;
-}
-
 constexpr int kGradThreads = 512;  // a TMEM quarter and a quarter of the columns per warp
 
 template <int P, int N>
@@ -264,8 +76,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
-    double *s_tw = reinterpret_cast<double *>(sm + L::oSum), *s_tot = s_tw + 8, *s_red = s_tot + 12;
-    float *s_rowp = reinterpret_cast<float *>(s_red + 16), *s_colp = s_rowp + 512, *s_diag = s_colp + 512, *s_wd = s_diag + 128,
+    double *s_tw = reinterpret_cast<double *>(sm + L::oSum);
+    float *s_tot = reinterpret_cast<float *>(s_tw + 8), *s_red = s_tot + 12, *s_rowp = s_red + 20, *s_colp = s_rowp + 512, *s_diag = s_colp + 512, *s_wd = s_diag + 128,
           *s_gxp = s_wd + 128, *s_syp = s_gxp + 512;
     uint64_t *bar_bc = reinterpret_cast<uint64_t *>(sm + L::oBar), *bar_x = bar_bc + 1, *bar_y = bar_bc + 2,
              *bar_s = bar_bc + 3, *bar_g = bar_bc + 4, *mma_bar = bar_bc + 5;
@@ -578,8 +390,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dot = fmaf(x[e] + y[e], st[i][e], dot);
             }
-            const double dd = ssm_warp_sum((double)dot);
-            if (lane == 0) s_red[warp] = dd;
+            dot = warp_sum(dot, 32);
+            if (lane == 0) s_red[warp] = dot;
         }
         mma_sync_point();
         if (*abort_flag) break;
@@ -614,14 +426,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 mma_bf16(tmem + tT, desc_k(sb + L::oB, kk), desc_mn(sb + L::oHi, kk, L::kSBlock), idesc_bf16(128, P, false, true),
                          kk > 0);
         }
-        double pre = 0.0, suf = 0.0, pre_in = 0.0, suf_in = 0.0, own = 0.0;
+        double pre = 0.0, suf = 0.0, pre_in = 0.0, suf_in = 0.0;
+        float own = 0.f;
         if (tid < 128) {
-            const double col = (double)s_colp[tid] + (double)s_colp[128 + tid] + (double)s_colp[256 + tid] + (double)s_colp[384 + tid];
-            const double gx = (double)s_gxp[tid] + (double)s_gxp[128 + tid] + (double)s_gxp[256 + tid] + (double)s_gxp[384 + tid];
-            const double rw = (double)s_rowp[tid] + (double)s_rowp[128 + tid] + (double)s_rowp[256 + tid] + (double)s_rowp[384 + tid];
-            suf = (double)s_syp[tid] + (double)s_syp[128 + tid] + (double)s_syp[256 + tid] + (double)s_syp[384 + tid];
-            own = col + (double)s_diag[tid] + gx;
-            pre = (double)s_dt[tid] * (col + gx) - rw;
+            const float cg = (s_colp[tid] + s_colp[128 + tid] + s_colp[256 + tid] + s_colp[384 + tid]) +
+                             (s_gxp[tid] + s_gxp[128 + tid] + s_gxp[256 + tid] + s_gxp[384 + tid]);
+            const float rw = s_rowp[tid] + s_rowp[128 + tid] + s_rowp[256 + tid] + s_rowp[384 + tid];
+            suf = (double)(s_syp[tid] + s_syp[128 + tid] + s_syp[256 + tid] + s_syp[384 + tid]);
+            own = cg + s_diag[tid];
+            pre = (double)fmaf(s_dt[tid], cg, -rw);  // the difference of the sums is what cancels: 64 bits from here
             pre_in = ssm_warp_scan(pre);
             suf_in = ssm_warp_scan(suf);
             if (lane == 31) {
@@ -650,24 +463,25 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             }
         }
         if (tid < 128) {
-            double cross = 0.0, before = pre_in - pre, after = -(suf_in - suf);
-            for (int w = 0; w < 16; ++w) cross += s_red[w];
+            double before = pre_in - pre, after = suf - suf_in;
+            float cross = lane < 16 ? s_red[lane] : 0.f;
             for (int w = 0; w < 4; ++w) {
                 if (w < warp) before += s_tw[w];
                 if (w >= warp) after += s_tw[4 + w];
             }
-            const double dlog = before + after + cross * (double)s_g[SsmGate::elast];
-            double raw = (own + (double)a.A[h] * dlog) * (double)s_g[SsmGate::sig + tid], sA = 0.0, sD = 0.0;
+            cross = warp_sum(cross, 32) * s_g[SsmGate::elast];
+            const float dlog = (float)(before + after + (double)cross);
+            float raw = fmaf(a.A[h], dlog, own) * s_g[SsmGate::sig + tid], sA = 0.f, sD = 0.f;
             if (tid < valid) {
-                a.ddelta[((size_t)b * a.T + t0 + tid) * a.H + h] = (float)raw;
-                sA = (double)s_dt[tid] * dlog;
-                sD = (double)s_wd[tid];
+                a.ddelta[((size_t)b * a.T + t0 + tid) * a.H + h] = raw;
+                sA = s_dt[tid] * dlog;
+                sD = s_wd[tid];
             } else {
-                raw = 0.0;
+                raw = 0.f;
             }
-            sA = ssm_warp_sum(sA);
-            raw = ssm_warp_sum(raw);
-            sD = ssm_warp_sum(sD);
+            sA = warp_sum(sA, 32);
+            raw = warp_sum(raw, 32);
+            sD = warp_sum(sD, 32);
             if (lane == 0) {
                 s_tot[warp * 3] = sA;
                 s_tot[warp * 3 + 1] = raw;
@@ -735,16 +549,16 @@ inline int ssm_grad_splits(int B, int T, int H, int G) {
     return best;
 }
 
-// Chunks per segment of the walk: rounds of chunks over the SMs' places (two a SM, both directions, halves of P);
-// a cut costs the segments' own states (as much again without the writes) and two launches.
-inline int ssm_walk_chunks(int B, int T, int H, int P) {
-    const int nch = (T + kTcQ - 1) / kTcQ, places = ssm_sm_count() * 2;
+// Chunks per segment of the walk: rounds of chunks over the SMs (one CTA each, both directions); a cut costs the
+// segments' own sums first (a chunk there about 0.8 of one with its states written) and three launches.
+inline int ssm_walk_chunks(int B, int T, int H) {
+    const int nch = (T + kTcQ - 1) / kTcQ, sms = ssm_sm_count();
     double best = 1e30;
     int at = nch;
     for (int m = nch; m >= 1; m = m > 64 ? m * 3 / 4 : m - 1) {
         const int R = (nch + m - 1) / m;
-        const double rounds = (double)((2LL * (P / 64) * B * H * R + places - 1) / places);
-        const double cost = R == 1 ? rounds * m : rounds * (2.0 * m + 1.0) + 6.0;
+        const double rounds = (double)((2LL * B * H * R + sms - 1) / sms);
+        const double cost = R == 1 ? rounds * (m + 2.0) : rounds * (1.8 * m + 4.0) + 6.0;
         if (cost < best * 0.999) {
             best = cost;
             at = m;
@@ -762,7 +576,7 @@ inline SsmTcBwdWs ssm_tc_bwd_ws(int B, int T, int H, int G, int P, int N) {
     const size_t units = (size_t)B * nch * H;
     SsmTcBwdWs w;
     w.splits = ssm_grad_splits(B, T, H, G);
-    w.m = ssm_walk_chunks(B, T, H, P);
+    w.m = ssm_walk_chunks(B, T, H);
     w.R = (nch + w.m - 1) / w.m;
     const size_t segs = w.R > 1 ? (size_t)B * w.R * H : 0;
     w.gates = 0;
@@ -796,20 +610,17 @@ cudaError_t ssm_tc_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
         !ssm_state_map(&ms, st, units, P, N) || !ssm_state_map(&mg, g, units, P, N))
         return cudaErrorInvalidValue;
     cudaError_t e = ssm_launch_gates(a, gates, s);
+    const dim3 grid(2u * (unsigned)(a.B * a.H) * (unsigned)w.R);
+    const size_t smem = SsmWalkTc<P, N>::kAlloc;
     if (e == cudaSuccess && w.R > 1) {
-        const dim3 grid((unsigned)(a.B * a.H) * (unsigned)w.R);
-        e = ssm_launch(ssm_tc_state_kernel<P, N, false>, grid, 256, (size_t)SsmStateTc<P, N, false>::kAlloc, s, mx, mb, a, w.m,
-                       (const float *)gates, segS, dec);
-        if (e == cudaSuccess)
-            e = ssm_launch(ssm_tc_state_kernel<P, N, true>, grid, 256, (size_t)SsmStateTc<P, N, true>::kAlloc, s, my, mc, a,
-                           w.m, (const float *)gates, segG, dec);
+        e = ssm_launch(ssm_tc_walk_kernel<P, N, false>, grid, SsmWalkTc<P, N>::kThreads, smem, s, mx, mb, my, mc, ms, mg, a, w.m, 2,
+                       (const float *)gates, segS, segG, dec);
         if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, w.R, a.H, P * N, segS, dec, a.S0, nullptr, s);
         if (e == cudaSuccess) e = ssm_launch_scan(true, a.B, w.R, a.H, P * N, segG, dec, a.dS_T, nullptr, s);
     }
     if (e == cudaSuccess)
-        e = ssm_launch(ssm_tc_walk_kernel<P, N>, dim3(2u * (P / 64) * (unsigned)(a.B * a.H) * (unsigned)w.R), 256,
-                       (size_t)SsmWalkTc<N>::kAlloc, s, mx, mb, my, mc, a, w.m, (const float *)gates,
-                       (const float *)segS, (const float *)segG, st, g);
+        e = ssm_launch(ssm_tc_walk_kernel<P, N, true>, grid, SsmWalkTc<P, N>::kThreads, smem, s, mx, mb, my, mc, ms, mg, a, w.m, 2,
+                       (const float *)gates, segS, segG, dec);
     const int per = (a.H / a.G + w.splits - 1) / w.splits;
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_grad_kernel<P, N>, dim3((unsigned)((size_t)a.B * nch * a.G * w.splits)), kGradThreads,

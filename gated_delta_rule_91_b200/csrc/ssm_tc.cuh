@@ -20,8 +20,7 @@
 //
 //   0. ssm_gate_kernel      the decays of every chunk and head as tables
 // A long sequence over few heads is cut into segments of whole chunks:
-//   1. ssm_tc_state_kernel  sum_j w_j x_j B_j^T of a segment (one product over
-//      its tokens: the weights reach to the segment's end)
+//   1. ssm_tc_walk_kernel   a segment's own sum of w_j x_j B_j^T, decayed to its end
 //   2. ssm_scan_kernel      the states between the segments, elementwise, fp32
 //   3. ssm_tc_y_kernel      walks its segment from that state
 // One segment alone is 0 and 3, with the state written at its end.
@@ -140,128 +139,247 @@ __global__ void __launch_bounds__(128) ssm_gate_kernel(SsmArgs a, float *__restr
     }
 }
 
-// ---- 1. segment states ------------------------------------------------------------------
-// BWD: sum_i e^{c_i} dy_i C_i^T with c from the segment's start.  out[b][seg][h][P][N], dec[b][seg][h].
-template <int P, int N, bool BWD>
-struct SsmStateTc {
-    static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile;
-    static constexpr uint32_t oX = 0, oB = XB, oHi = oB + BB, oLo = oHi + BB, oZero = oLo + BB;
-    static constexpr uint32_t kHiBlock = N == 64 ? 2 * kTile : kTile;  // distance of the second 64 lanes
-    static constexpr uint32_t oGate = oZero + (N == 64 ? kTile : 0);
-    static constexpr uint32_t oCtl = oGate + SsmGate::kFwdBytes;
-    static constexpr uint32_t kAlloc = oCtl + 64 + 1024;
+// ---- 1. walks over the chunks ------------------------------------------------------------
+// A state's two bf16 parts in memory: [unit][part][N][P], unit = (b, chunk, head).
+inline bool ssm_state_map(CUtensorMap *map, const void *base, size_t units, int P, int N) {
+    SsmEncodeFn enc = ssm_encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)P, (cuuint64_t)N, 2, (cuuint64_t)units};
+    const cuuint64_t strides[3] = {(cuuint64_t)P * 2, (cuuint64_t)N * P * 2, (cuuint64_t)2 * N * P * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)N, 1, 1}, estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A CTA walks the chunks of one (b, h, segment), forwards (S <- e^{c_last} S + (w B)^T X) or, rev, backwards (G <-
+// e^{c_last} G + (e^c C)^T dY), the state in TMEM (lanes n, columns p, fp32), the weighted rows in two bf16 parts.
+// OUT: from the state that enters the segment, every chunk's entering state is written as two bf16 parts (out_S, out_G
+// through tm_s, tm_g), and dS0 at the end.  Otherwise: from zero, the segment's own sum goes to seg_S or seg_G
+// [b][seg][h][P][N] in fp32, and its decay to dec.
+// Two stages of operands: while a chunk's products run, the next chunk's rows are weighted (a chunk takes about 2500
+// cycles; with one stage and half the warps it took 4500, or 9400 where the states were stored row by row).
+template <int P, int N>
+struct SsmWalkTc {
+    static constexpr int kThreads = 512, PW = P / 4;
+    static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile, kStage = XB + 2 * BB;
+    static constexpr uint32_t oX = 0, oHi = XB, oLo = XB + BB, oZero = 2 * kStage;
+    static constexpr uint32_t kSBlock = N * 128, SB = P / 64 * kSBlock;  // a state part as a tile: N rows
+    static constexpr uint32_t oGate = oZero + (N == 64 ? kTile : 0);     // two tables
+    static constexpr uint32_t oCtl = oGate + 2 * SsmGate::kFwdBytes;
+    static constexpr uint32_t kAlloc = oCtl + 96 + 1024;
 };
 
-template <int P, int N, bool BWD>
-__global__ void __launch_bounds__(256) ssm_tc_state_kernel(const __grid_constant__ CUtensorMap tm_x,
-                                                           const __grid_constant__ CUtensorMap tm_b, SsmArgs a, int m,
-                                                           const float *__restrict__ gates, float *__restrict__ out,
-                                                           float *__restrict__ dec) {
-    using L = SsmStateTc<P, N, BWD>;
+template <int P, int N, bool OUT>
+__global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
+    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
+    const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_c,
+    const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_g, SsmArgs a, int m, int dirs,
+    const float *__restrict__ gates, float *__restrict__ seg_S, float *__restrict__ seg_G, float *__restrict__ dec) {
+    using L = SsmWalkTc<P, N>;
     using namespace sm100;
+    constexpr int PW = L::PW;
+    constexpr bool kBoth = P == 64;  // both parts of a state fit a stage's second-part buffer
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
-    const float *s_g = reinterpret_cast<const float *>(sm + L::oGate);
-    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(sm + L::oCtl), *mma_bar = tma_bar + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tma_bar + 2);
+    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(sm + L::oCtl), *bar_g = tma_bar + 2, *mma_bar = tma_bar + 4;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tma_bar + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int q = warp & 3, prt = warp >> 2, row = q * 32 + lane, cp = prt * PW;  // state row n, first column p
     const int nch = (a.T + kTcQ - 1) / kTcQ, R = (nch + m - 1) / m;
-    const int seg = blockIdx.x % R, bh = blockIdx.x / R, h = bh % a.H, b = bh / a.H, g = h / (a.H / a.G);
+    int u = blockIdx.x;
+    const bool rev = dirs == 2 && (u & 1);
+    if (dirs == 2) u >>= 1;
+    const int seg = u % R, bh = u / R, h = bh % a.H, b = bh / a.H, g = h / (a.H / a.G);
     const int c0 = seg * m, cn = min(m, nch - c0);
+    auto chunk = [&](int k) { return rev ? c0 + cn - 1 - k : c0 + k; };
 
     if (tid == 0) {
-        mbar_init(tma_bar, 1);
-        mbar_init(mma_bar, 1);
+        for (int i = 0; i < 5; ++i) mbar_init(tma_bar + i, 1);
         fence_mbar_init();
         *abort_flag = 0;
     }
     if (warp == 0) tmem_alloc(tmem_slot, P);
     if (N == 64)
-        for (int i = tid; i < (int)kTile / 16; i += 256) reinterpret_cast<uint4 *>(sm + L::oZero)[i] = make_uint4(0, 0, 0, 0);
-    fence_async_smem();
+        for (int i = tid; i < (int)kTile / 16; i += 512) reinterpret_cast<uint4 *>(sm + L::oZero)[i] = make_uint4(0, 0, 0, 0);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = *tmem_slot;
-
-    // forward: chunks from the last, so that the decay to the segment's end is known; backward: from the first
-    auto chunk = [&](int k) { return BWD ? c0 + k : c0 + cn - 1 - k; };
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + cp;
+    constexpr int kIo = 128;  // the thread that issues copies; thread 0 issues products
     auto issue = [&](int k) {
-        mbar_expect_tx(tma_bar, L::XB + L::BB + SsmGate::kFwdBytes);
-        bulk_load_g2s(sm + L::oGate, gates + (((size_t)b * nch + chunk(k)) * a.H + h) * SsmGate::stride, SsmGate::kFwdBytes,
-                      tma_bar);
-        for (int i = 0; i < P / 64; ++i) tma_load_4d(sm + L::oX + i * kTile, &tm_x, tma_bar, i * 64, h, chunk(k) * kTcQ, b);
-        for (int i = 0; i < N / 64; ++i) tma_load_4d(sm + L::oB + i * kTile, &tm_b, tma_bar, i * 64, g, chunk(k) * kTcQ, b);
+        uint8_t *st = sm + (k & 1) * L::kStage;
+        mbar_expect_tx(tma_bar + (k & 1), L::XB + L::BB);
+        for (int i = 0; i < P / 64; ++i)
+            tma_load_4d(st + L::oX + i * kTile, rev ? &tm_dy : &tm_x, tma_bar + (k & 1), i * 64, h, chunk(k) * kTcQ, b);
+        for (int i = 0; i < N / 64; ++i)
+            tma_load_4d(st + L::oHi + i * kTile, rev ? &tm_c : &tm_b, tma_bar + (k & 1), i * 64, g, chunk(k) * kTcQ, b);
     };
-    if (tid == 0) issue(0);
-    double edge = 0.0;  // log2 decay between this chunk and the segment's end (start for BWD)
-    bool pending = false;
+    auto issue_g = [&](int k) {
+        mbar_expect_tx(bar_g + (k & 1), SsmGate::kFwdBytes);
+        bulk_load_g2s(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes,
+                      gates + (((size_t)b * nch + chunk(k)) * a.H + h) * SsmGate::stride, SsmGate::kFwdBytes, bar_g + (k & 1));
+    };
+    int n_t = 0, n_g = 0;  // issued, by that thread
+    if (tid == kIo)
+        for (int k = 0; k < 2 && k < cn; ++k) {
+            issue_g(k);
+            issue(k);
+            n_t = n_g = k + 1;
+        }
+    __syncwarp();
+    // every thread: the chunk's rows weighted in place, the second part beside them
+    auto convert = [&](int k) {
+        const uint32_t par = (uint32_t)(k >> 1) & 1;
+        if (!mbar_wait(bar_g + (k & 1), par) || !mbar_wait(tma_bar + (k & 1), par)) {
+            *abort_flag = 1;
+            return;
+        }
+        const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes);
+        uint8_t *st = sm + (k & 1) * L::kStage;
+        const int r = tid & 127;
+        const float w = rev ? s_g[SsmGate::e + r] : s_g[SsmGate::dt + r] * s_g[SsmGate::el + r];
+        constexpr int CH = N / 32;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = (tid >> 7) * CH + i;
+            const uint32_t off = (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
+            float x[8];
+            ld8s(st + L::oHi + off, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= w;
+            st_split8(st + L::oHi + off, st + L::oLo + off, x);
+        }
+    };
+    float v[PW];
+    {
+        const float *src = nullptr;
+        if (OUT) {
+            if (R > 1) src = (rev ? seg_G : seg_S) + (((size_t)b * R + seg) * a.H + h) * P * N;
+            else if (rev ? a.dS_T : a.S0) src = (rev ? a.dS_T : a.S0) + (size_t)bh * P * N;
+        }
+#pragma unroll
+        for (int i = 0; i < PW; ++i) v[i] = src && row < N ? src[(size_t)(cp + i) * N + row] : 0.f;
+        tmem_stw<PW>(tl, v);
+        tmem_wait_st();
+    }
+    convert(0);
+    fence_async_smem();
+    tc_before_sync();
+    __syncthreads();
+    double edge = 0.0;
+    const bool keep = !OUT || (rev && seg == 0 && a.dS0);  // the state behind the last chunk is an output
+    bool mma_open = false;
     int k = 0;
 #pragma unroll 1
-    for (; k < cn; ++k) {
-        if (tid == 0 && !mbar_wait(tma_bar, (uint32_t)(k & 1))) *abort_flag = 1;
-        __syncthreads();
-        if (*abort_flag) break;
-        {   // the weighted rows in two bf16 parts: row tid & 127, half of the columns
-            const int r = tid & 127, half = tid >> 7;
-            const float far = exp2f((float)edge);
-            const float w = BWD ? s_g[SsmGate::e + r] * far : s_g[SsmGate::dt + r] * s_g[SsmGate::el + r] * far;
-            edge += *reinterpret_cast<const double *>(s_g + SsmGate::last);
-            constexpr int CH = N / 16;  // 16-byte chunks of a half row
+    for (; k < cn && !*abort_flag; ++k) {
+        const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes);
+        uint8_t *free_lo = sm + ((k + 1) & 1) * L::kStage + L::oLo;  // last read by the products of the chunk before
+        const float el = s_g[SsmGate::elast];
+        const bool update = keep || k + 1 < cn;
+        edge += *reinterpret_cast<const double *>(s_g + SsmGate::last);
+        if (tid == kIo && k > 0 && k + 1 < cn) {
+            issue(k + 1);
+            n_t = k + 2;
+        }
+        __syncwarp();
+        float lo[PW];
+        if (row < N) {
+            tmem_ldw<PW>(tl, v);
+            if (OUT) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = half * CH + i;
-                const uint32_t off = (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
-                float v[8];
-                ld8s(sm + L::oB + off, v);
+                for (int i = 0; i < PW; ++i) lo[i] = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= w;
-                st_split8(sm + L::oHi + off, sm + L::oLo + off, v);
+                for (int i = 0; i < PW / 8; ++i) {
+                    const uint32_t off = (uint32_t)(cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i);
+                    st_bf16x8(free_lo + off, v + 8 * i);
+                    if (kBoth) st_bf16x8(free_lo + L::SB + off, lo + 8 * i);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < PW; ++i) v[i] *= el;
+            tmem_stw<PW>(tl, v);
+            tmem_wait_st();
         }
         fence_async_smem();
+        tc_before_sync();
         __syncthreads();
-        if (tid == 0) {
+        const int unit = (int)(((size_t)b * nch + chunk(k)) * a.H + h);
+        if (OUT && tid == kIo) {
+            for (int pt = 0; pt < (kBoth ? 2 : 1); ++pt)
+                for (int i = 0; i < P / 64; ++i)
+                    tma_store_4d(rev ? &tm_g : &tm_s, free_lo + pt * L::SB + i * L::kSBlock, i * 64, 0, pt, unit);
+            bulk_commit();
+        }
+        if (tid == 0 && update) {
             tc_after_sync();
+            const uint32_t st = sb + (k & 1) * L::kStage;
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < 2; ++part) {
+                const uint32_t at = st + (part ? L::oLo : L::oHi);
+                const uint32_t block = N == 64 ? sb + L::oZero - at : kTile;  // the second 64 lanes
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16(tmem, desc_mn(sb + (part ? L::oLo : L::oHi), kk, part ? kTile : L::kHiBlock),
-                             desc_mn(sb + L::oX, kk), idesc_bf16(128, P, true, true), k > 0 || part > 0 || kk > 0);
+                    mma_bf16(tmem, desc_mn(at, kk, block), desc_mn(st + L::oX, kk),
+                             idesc_bf16(128, P, true, true), 1);
+            }
             mma_commit(mma_bar);
-            if (!mbar_wait(mma_bar, (uint32_t)(k & 1))) {
-                *abort_flag = 1;
-                pending = true;
-            } else if (k + 1 < cn) {
-                issue(k + 1);
+        }
+        __syncwarp();
+        if (OUT) {
+            if (tid == kIo) bulk_wait_read_all();
+            __syncthreads();
+            if (!kBoth) {
+                if (row < N)
+#pragma unroll
+                    for (int i = 0; i < PW / 8; ++i)
+                        st_bf16x8(free_lo + (uint32_t)(cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i), lo + 8 * i);
+                fence_async_smem();
+                __syncthreads();
+                if (tid == kIo) {
+                    for (int i = 0; i < P / 64; ++i)
+                        tma_store_4d(rev ? &tm_g : &tm_s, free_lo + i * L::kSBlock, i * 64, 0, 1, unit);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                }
+                __syncthreads();
             }
         }
+        if (k + 1 < cn) convert(k + 1);
+        fence_async_smem();
+        if (tid == 0 && update) {
+            mma_open = !mbar_wait(mma_bar, (uint32_t)(k & 1));
+            if (mma_open) *abort_flag = 1;
+        }
+        tc_before_sync();
         __syncthreads();
-        if (*abort_flag) break;
+        tc_after_sync();
+        if (tid == kIo && k + 2 < cn) {  // this chunk's table is done with
+            issue_g(k + 2);
+            n_g = k + 3;
+        }
+        __syncwarp();
     }
     if (*abort_flag) {
-        if (tid == 0) {
+        if (tid == kIo) {
             record_status(GDR_ERR_TIMEOUT);
-            // one wait more for what is still in flight: the chunk's copies, or its products
-            mbar_wait(pending ? mma_bar : tma_bar, (uint32_t)(k & 1));
+            for (int i = n_t > 1 ? n_t - 2 : 0; i < n_t; ++i) mbar_wait(tma_bar + (i & 1), (uint32_t)(i >> 1) & 1);
+            for (int i = n_g > 1 ? n_g - 2 : 0; i < n_g; ++i) mbar_wait(bar_g + (i & 1), (uint32_t)(i >> 1) & 1);
+            if (OUT) bulk_wait_all();
         }
+        if (tid == 0 && mma_open) mbar_wait(mma_bar, (uint32_t)((k - 1) & 1));
     } else {
-        tc_after_sync();
-        const int n = (warp & 3) * 32 + (tid & 31), half = warp >> 2;
-        const size_t unit = ((size_t)b * R + seg) * a.H + h;
-        if ((warp & 3) * 32 < N) {
-#pragma unroll 1
-            for (int c = half * (P / 2); c < (half + 1) * (P / 2); c += 32) {
-                float v[32];
-                tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
+        if (keep && row < N) {
+            float *dst = OUT ? a.dS0 + (size_t)bh * P * N : (rev ? seg_G : seg_S) + (((size_t)b * R + seg) * a.H + h) * P * N;
+            tmem_ldw<PW>(tl, v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) out[(unit * P + c + i) * N + n] = v[i];
-            }
+            for (int i = 0; i < PW; ++i) dst[(size_t)(cp + i) * N + row] = v[i];
         }
-        if (!BWD && tid == 0) dec[unit] = exp2f((float)edge);
+        if (!OUT && !rev && tid == 0) dec[((size_t)b * R + seg) * a.H + h] = exp2f((float)edge);
+        if (OUT && tid == kIo) bulk_wait_all();
     }
     tc_before_sync();
     __syncthreads();
@@ -621,8 +739,8 @@ cudaError_t ssm_tc_fwd(const SsmArgs &a, void *ws, cudaStream_t s) {
                           mb, mc, a, m, (const float *)gates, (const float *)nullptr);
     float *st = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.st);
     float *dec = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.dec);
-    e = ssm_launch(ssm_tc_state_kernel<P, N, false>, grid, 256, (size_t)SsmStateTc<P, N, false>::kAlloc, s, mx, mb, a, m,
-                   (const float *)gates, st, dec);
+    e = ssm_launch(ssm_tc_walk_kernel<P, N, false>, grid, SsmWalkTc<P, N>::kThreads, (size_t)SsmWalkTc<P, N>::kAlloc, s, mx, mb,
+                   mx, mb, mx, mx, a, m, 1, (const float *)gates, st, (float *)nullptr, dec);
     if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, R, a.H, P * N, st, dec, a.S0, a.S_T, s);
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_y_kernel<P, N, false>, grid, SsmYTc<P, N, false>::NT, (size_t)SsmYTc<P, N, false>::kAlloc, s, mx,

@@ -145,6 +145,13 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
         "r"(smem_u32(bar))
         : "memory");
 }
+// The same tile into L2 only.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
 // Tiled TMA store from this CTA's shared memory (tracked by bulk async-groups);
 // coordinates past the tensor's extent are not written.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int x, int y,

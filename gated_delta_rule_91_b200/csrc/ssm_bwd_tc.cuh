@@ -114,9 +114,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     constexpr uint32_t tK = 0, tT = 128, tC = 256, tB = 256 + N;
 
-    int n_x = 0, n_y = 0, n_s = 0, n_g = 0;  // issued, by thread 0
+    constexpr int kIo = 384;              // issues copies (a warp above the diagonal); thread 0 issues products
+    int n_x = 0, n_y = 0, n_s = 0, n_g = 0;  // issued, by that thread
     uint32_t s_phase = 0;                             // everyone's
-    bool bc_open = false, mma_open = false;
+    bool mma_open = false;
     auto issue_x = [&](int h) {
         mbar_expect_tx(bar_x, L::XB);
         for (int i = 0; i < P / 64; ++i) tma_load_4d(sm + L::oX + i * kTile, &tm_x, bar_x, i * 64, h, t0, b);
@@ -144,21 +145,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         if (!mbar_wait(bar_s, s_phase)) *abort_flag = 1;
         s_phase ^= 1;
     };
-    if (tid == 0) {
+    if (tid == kIo) {
         mbar_expect_tx(bar_bc, 2 * L::BB);
         for (int i = 0; i < N / 64; ++i) {
             tma_load_4d(sm + L::oB + i * kTile, &tm_b, bar_bc, i * 64, g, t0, b);
             tma_load_4d(sm + L::oC + i * kTile, &tm_c, bar_bc, i * 64, g, t0, b);
         }
-        bc_open = true;
         issue_x(h0);
         issue_y(h0);
         issue_g(0);
     }
     uint32_t mma_phase = 0;
-    auto mma_sync_point = [&]() {
+    auto mma_sync_point = [&]() {  // thread 0 has committed its products
         if (tid == 0) {
-            mma_commit(mma_bar);
             mma_open = !mbar_wait(mma_bar, mma_phase);
             if (mma_open) *abort_flag = 1;
         }
@@ -183,17 +182,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             prefetch_l2(reinterpret_cast<const uint8_t *>(Gout) + unit * 4 * P * N + tid * 128);
         }
         if (tid == 0) {
-            if (bc_open) {
-                if (!mbar_wait(bar_bc, 0)) *abort_flag = 1;
-                else bc_open = false;
-            }
+            if (hh == 0 && !mbar_wait(bar_bc, 0)) *abort_flag = 1;
             if (!mbar_wait(bar_g, (uint32_t)(hh & 1)) || !mbar_wait(bar_x, (uint32_t)(hh & 1)) ||
                 !mbar_wait(bar_y, (uint32_t)(hh & 1)))
                 *abort_flag = 1;
         }
         __syncthreads();
         if (*abort_flag) break;
-        if (tid == 0 && hh + 1 < nh) issue_g(hh + 1);  // the other table was last read a head ago
+        if (tid == kIo && hh + 1 < nh) issue_g(hh + 1);  // the other table was last read a head ago
         __syncwarp();
         // ---- W = dY X^T (and once K = C B^T) ----
         if (tid == 0) {
@@ -205,6 +201,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
 #pragma unroll
             for (int kk = 0; kk < P / 16; ++kk)
                 mma_bf16(tmem + tT, desc_k(sb + L::oY, kk), desc_k(sb + L::oX, kk), idesc_bf16(128, 128, false, false), kk > 0);
+            mma_commit(mma_bar);
         }
         mma_sync_point();
         if (*abort_flag) break;
@@ -227,20 +224,30 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 tmem_ld32(tl + tT + prt * 32, wv);
                 if (prt < q) {
                     const float rf = s_g[SsmGate::rowf + row];
+                    const float2 rf2 = make_float2(rf, rf);
+                    float2 sum2 = make_float2(0.f, 0.f);
                     const float4 *col4 = reinterpret_cast<const float4 *>(s_g + SsmGate::col + (q - 1) * 96 + prt * 32);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float4 c4 = col4[i], d4 = dt4[i];
-                        const float l[4] = {rf * c4.x, rf * c4.y, rf * c4.z, rf * c4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
+                        const float2 c2[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+                        const float2 d2[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int n = 4 * i + u;
-                            kv[n] *= l[u];
-                            rr[n] = kv[n] * wv[n];
-                            rsum = fmaf(rr[n], d[u], rsum);
-                            wv[n] *= l[u] * d[u];
+                        for (int u = 0; u < 2; ++u) {
+                            const int n = 4 * i + 2 * u;
+                            const float2 l = fmul2(rf2, c2[u]), w = make_float2(wv[n], wv[n + 1]);
+                            const float2 kk = fmul2(make_float2(kv[n], kv[n + 1]), l), r = fmul2(kk, w);
+                            const float2 dk2 = fmul2(w, fmul2(l, d2[u]));
+                            sum2 = ffma2(r, d2[u], sum2);
+                            kv[n] = kk.x;
+                            kv[n + 1] = kk.y;
+                            rr[n] = r.x;
+                            rr[n + 1] = r.y;
+                            wv[n] = dk2.x;
+                            wv[n + 1] = dk2.y;
                         }
                     }
+                    rsum = sum2.x + sum2.y;
                 } else {
                     const float ci = s_g[SsmGate::hi + row], cl = s_g[SsmGate::lo + row];
                     const float4 *hi4 = reinterpret_cast<const float4 *>(s_g + SsmGate::hi + prt * 32);
@@ -293,6 +300,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             for (int kk = 0; kk < 8; ++kk)
                 mma_bf16(tmem + tB, desc_mn(sb + L::oK, kk), desc_mn(sb + L::oC, kk), idesc_bf16(128, N, true, true),
                          hh > 0 || kk > 0);
+            mma_commit(mma_bar);
         }
         __syncwarp();
         if (prt <= q) {  // the sums of R, beside the products
@@ -304,12 +312,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         s_rowp[prt * 128 + row] = rsum;
         mma_sync_point();
         if (*abort_flag) break;
-        if (tid == 0) issue_state(&tm_s, unit);  // over M' and dK
+        if (tid == kIo) issue_state(&tm_s, unit);  // over M' and dK
         __syncwarp();
         float dxi[PW];  // Delta dXi + D dy
         tmem_ldw<PW>(tl + tT + prt * PW, dxi);
         {
-            const float dt = s_dt[row], D = a.D ? a.D[h] : 0.f;
+            const float dt = s_dt[row], D = s_g[SsmGate::D];
             const int c = prt * PW;
 #pragma unroll
             for (int i = 0; i < PW / 8; ++i) {
@@ -331,7 +339,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 for (int kk = 0; kk < P / 16; ++kk)
                     mma_bf16(tmem + tT, desc_k(sb + L::oY, kk), desc_k(sb + (pt ? L::oLo : L::oHi), kk, L::kSBlock),
                              idesc_bf16(128, N, false, false), pt > 0 || kk > 0);
+            mma_commit(mma_bar);
         }
+        __syncwarp();
         float st[kChunks][8];
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         mma_sync_point();
         if (*abort_flag) break;
-        if (tid == 0) {
+        if (tid == kIo) {
             issue_state(&tm_g, unit);
             if (hh + 1 < nh) issue_y(h + 1);
         }
@@ -379,7 +389,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 for (int kk = 0; kk < P / 16; ++kk)
                     mma_bf16(tmem + tT, desc_k(sb + L::oX, kk), desc_k(sb + (pt ? L::oLo : L::oHi), kk, L::kSBlock),
                              idesc_bf16(128, N, false, false), pt > 0 || kk > 0);
+            mma_commit(mma_bar);
         }
+        __syncwarp();
         {
             float dot = 0.f;  // <G, S_in>, each from its two parts
 #pragma unroll
@@ -395,7 +407,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         mma_sync_point();
         if (*abort_flag) break;
-        if (tid == 0 && hh + 1 < nh) issue_x(h + 1);
+        if (tid == kIo && hh + 1 < nh) issue_x(h + 1);
         __syncwarp();
         {
             const float el = s_g[SsmGate::el + row], w = el * s_dt[row];
@@ -418,33 +430,58 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         tc_before_sync();
         __syncthreads();
-        // ---- T = B G_out^T; beside it the per-token sums of this head: token tid ----
+        // ---- T = B G_out^T; beside it the per-token sums of this head, a token a thread of warps 4-7 ----
         if (tid == 0) {
             tc_after_sync();
 #pragma unroll
             for (int kk = 0; kk < N / 16; ++kk)
                 mma_bf16(tmem + tT, desc_k(sb + L::oB, kk), desc_mn(sb + L::oHi, kk, L::kSBlock), idesc_bf16(128, P, false, true),
                          kk > 0);
+            mma_commit(mma_bar);
         }
-        double pre = 0.0, suf = 0.0, pre_in = 0.0, suf_in = 0.0;
-        float own = 0.f;
-        if (tid < 128) {
-            const float cg = (s_colp[tid] + s_colp[128 + tid] + s_colp[256 + tid] + s_colp[384 + tid]) +
-                             (s_gxp[tid] + s_gxp[128 + tid] + s_gxp[256 + tid] + s_gxp[384 + tid]);
-            const float rw = s_rowp[tid] + s_rowp[128 + tid] + s_rowp[256 + tid] + s_rowp[384 + tid];
-            suf = (double)(s_syp[tid] + s_syp[128 + tid] + s_syp[256 + tid] + s_syp[384 + tid]);
-            own = cg + s_diag[tid];
-            pre = (double)fmaf(s_dt[tid], cg, -rw);  // the difference of the sums is what cancels: 64 bits from here
-            pre_in = ssm_warp_scan(pre);
-            suf_in = ssm_warp_scan(suf);
+        __syncwarp();
+        if (warp >= 4 && warp < 8) {
+            const int t = tid - 128, w4 = warp - 4;
+            const float cg = (s_colp[t] + s_colp[128 + t] + s_colp[256 + t] + s_colp[384 + t]) +
+                             (s_gxp[t] + s_gxp[128 + t] + s_gxp[256 + t] + s_gxp[384 + t]);
+            const float rw = s_rowp[t] + s_rowp[128 + t] + s_rowp[256 + t] + s_rowp[384 + t], dt = s_dt[t];
+            const double suf = (double)(s_syp[t] + s_syp[128 + t] + s_syp[256 + t] + s_syp[384 + t]);
+            const double pre = (double)fmaf(dt, cg, -rw);  // the difference of the sums is what cancels: 64 bits from here
+            const double pre_in = ssm_warp_scan(pre), suf_in = ssm_warp_scan(suf);
             if (lane == 31) {
-                s_tw[warp] = pre_in;
-                s_tw[4 + warp] = suf_in;
+                s_tw[w4] = pre_in;
+                s_tw[4 + w4] = suf_in;
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            double before = pre_in - pre, after = suf - suf_in;
+            float cross = lane < 16 ? s_red[lane] : 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (w < w4) before += s_tw[w];
+                if (w >= w4) after += s_tw[4 + w];
+            }
+            cross = warp_sum(cross, 32) * s_g[SsmGate::elast];
+            const float dlog = (float)(before + after + (double)cross);
+            float raw = fmaf(s_g[SsmGate::A], dlog, cg + s_diag[t]) * s_g[SsmGate::sig + t], sA = 0.f, sD = 0.f;
+            if (t < valid) {
+                a.ddelta[((size_t)b * a.T + t0 + t) * a.H + h] = raw;
+                sA = dt * dlog;
+                sD = s_wd[t];
+            } else {
+                raw = 0.f;
+            }
+            sA = warp_sum(sA, 32);
+            raw = warp_sum(raw, 32);
+            sD = warp_sum(sD, 32);
+            if (lane == 0) {
+                s_tot[w4 * 3] = sA;
+                s_tot[w4 * 3 + 1] = raw;
+                s_tot[w4 * 3 + 2] = sD;
             }
         }
         mma_sync_point();
         if (*abort_flag) break;
-        // ---- dx (a thread's columns of its row), and the end of the token sums ----
+        // ---- dx: a thread's columns of its row ----
         {
             const float w = s_g[SsmGate::el + row] * s_dt[row];
             const int c = prt * PW;
@@ -462,45 +499,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 }
             }
         }
-        if (tid < 128) {
-            double before = pre_in - pre, after = suf - suf_in;
-            float cross = lane < 16 ? s_red[lane] : 0.f;
-            for (int w = 0; w < 4; ++w) {
-                if (w < warp) before += s_tw[w];
-                if (w >= warp) after += s_tw[4 + w];
-            }
-            cross = warp_sum(cross, 32) * s_g[SsmGate::elast];
-            const float dlog = (float)(before + after + (double)cross);
-            float raw = fmaf(a.A[h], dlog, own) * s_g[SsmGate::sig + tid], sA = 0.f, sD = 0.f;
-            if (tid < valid) {
-                a.ddelta[((size_t)b * a.T + t0 + tid) * a.H + h] = raw;
-                sA = s_dt[tid] * dlog;
-                sD = s_wd[tid];
-            } else {
-                raw = 0.f;
-            }
-            sA = warp_sum(sA, 32);
-            raw = warp_sum(raw, 32);
-            sD = warp_sum(sD, 32);
-            if (lane == 0) {
-                s_tot[warp * 3] = sA;
-                s_tot[warp * 3 + 1] = raw;
-                s_tot[warp * 3 + 2] = sD;
-            }
-        }
         tc_before_sync();
         __syncthreads();
         if (tid < 3) part[tid * units + unit] = (float)(s_tot[tid] + s_tot[3 + tid] + s_tot[6 + tid] + s_tot[9 + tid]);
     }
     if (*abort_flag) {
-        if (tid == 0) {
+        if (tid == 0 && mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
+        if (tid == kIo) {
             record_status(GDR_ERR_TIMEOUT);
-            if (bc_open) mbar_wait(bar_bc, 0);
+            mbar_wait(bar_bc, 0);
             mbar_wait(bar_x, (uint32_t)((n_x - 1) & 1));
             mbar_wait(bar_y, (uint32_t)((n_y - 1) & 1));
             mbar_wait(bar_g, (uint32_t)((n_g - 1) & 1));
             if (n_s > 0) mbar_wait(bar_s, (uint32_t)((n_s - 1) & 1));
-            if (mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
         }
     } else {
         tc_after_sync();

@@ -94,6 +94,7 @@ struct SsmGate {
     static constexpr int dt = 0, e = 128, rowf = 256, el = 384, hi = 512, lo = 640;  // per token, see below
     static constexpr int col = 768;                       // [I-1][96]: 2^{r_I - c_j} of the blocks I = 1..3, j < 32 I
     static constexpr int last = 1056, elast = 1058;       // c_last (a double) and 2^{c_last}
+    static constexpr int A = 1059, D = 1060;              // the head's (D: 0 without one)
     static constexpr int sig = 1072, stride = 1200;       // d softplus / dz
     static constexpr uint32_t kFwdBytes = sig * 4, kBytes = stride * 4;
 };
@@ -136,6 +137,8 @@ __global__ void __launch_bounds__(128) ssm_gate_kernel(SsmArgs a, float *__restr
     if (t == 0) {
         *reinterpret_cast<double *>(out + SsmGate::last) = last;
         out[SsmGate::elast] = exp2f((float)last);
+        out[SsmGate::A] = a.A[h];
+        out[SsmGate::D] = a.D ? a.D[h] : 0.f;
     }
 }
 
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     tc_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + cp;
-    constexpr int kIo = 128;  // the thread that issues copies; thread 0 issues products
+    constexpr int kIo = 384;  // the thread that issues copies; thread 0 issues products
     auto issue = [&](int k) {
         uint8_t *st = sm + (k & 1) * L::kStage;
         mbar_expect_tx(tma_bar + (k & 1), L::XB + L::BB);
@@ -223,12 +226,18 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         bulk_load_g2s(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes,
                       gates + (((size_t)b * nch + chunk(k)) * a.H + h) * SsmGate::stride, SsmGate::kFwdBytes, bar_g + (k & 1));
     };
+    auto prefetch = [&](int k) {  // two stages leave less than a load's latency
+        if (k >= cn) return;
+        for (int i = 0; i < P / 64; ++i) tma_prefetch_4d(rev ? &tm_dy : &tm_x, i * 64, h, chunk(k) * kTcQ, b);
+        for (int i = 0; i < N / 64; ++i) tma_prefetch_4d(rev ? &tm_c : &tm_b, i * 64, g, chunk(k) * kTcQ, b);
+    };
     int n_t = 0, n_g = 0;  // issued, by that thread
     if (tid == kIo)
         for (int k = 0; k < 2 && k < cn; ++k) {
             issue_g(k);
             issue(k);
             n_t = n_g = k + 1;
+            prefetch(k + 2);
         }
     __syncwarp();
     // every thread: the chunk's rows weighted in place, the second part beside them
@@ -284,6 +293,7 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         if (tid == kIo && k > 0 && k + 1 < cn) {
             issue(k + 1);
             n_t = k + 2;
+            prefetch(k + 3);
         }
         __syncwarp();
         float lo[PW];
@@ -461,13 +471,25 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
         bulk_load_g2s(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes,
                       gates + (((size_t)b * nch + c0 + k) * a.H + h) * SsmGate::stride, SsmGate::kFwdBytes, bar_g);
     };
-    int n_bc = 0, n_x = 0, n_g = 0;  // issued, by thread 0
-    if (tid == 0) {
+    auto prefetch = [&](int k) {
+        if (k >= cn) return;
+        for (int i = 0; i < P / 64; ++i) tma_prefetch_4d(&tm_x, i * 64, h, (c0 + k) * kTcQ, b);
+        for (int i = 0; i < N / 64; ++i) {
+            tma_prefetch_4d(&tm_b, i * 64, g, (c0 + k) * kTcQ, b);
+            tma_prefetch_4d(&tm_c, i * 64, g, (c0 + k) * kTcQ, b);
+        }
+    };
+    // Copies are issued by a warp whose scores are mostly above the diagonal, products by thread 0.
+    constexpr int kIo = L::NT - 128;
+    int n_bc = 0, n_x = 0, n_g = 0;  // issued, by that thread
+    if (tid == kIo) {
         issue_g(0);
         issue_bc(0);
         issue_x(0);
         n_bc = n_x = n_g = 1;
+        prefetch(1);
     }
+    __syncwarp();
     {   // the entering state: lane n, columns p
         const float *src = states ? states + (((size_t)b * R + seg) * a.H + h) * P * N : a.S0 ? a.S0 + (size_t)bh * P * N : nullptr;
         float v[32];
@@ -478,9 +500,8 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
     }
     uint32_t mma_phase = 0;
     bool mma_open = false;
-    auto mma_sync_point = [&]() {
+    auto mma_sync_point = [&]() {  // thread 0 has committed its products
         if (tid == 0) {
-            mma_commit(mma_bar);
             mma_open = !mbar_wait(mma_bar, mma_phase);
             if (mma_open) *abort_flag = 1;
         }
@@ -498,7 +519,7 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
         }
         __syncthreads();
         if (*abort_flag) break;
-        if (tid == 0 && k + 1 < cn) {  // the other table was last read a chunk ago
+        if (tid == kIo && k + 1 < cn) {  // the other table was last read a chunk ago
             issue_g(k + 1);
             ++n_g;
         }
@@ -529,6 +550,7 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
             for (int kk = 0; kk < N / 16; ++kk)
                 mma_bf16(tmem + tY2, desc_k(sb + L::oC, kk), desc_mn(sb + L::oS, kk, L::kSBlock),
                          idesc_bf16(128, P, false, true), kk > 0);
+            mma_commit(mma_bar);
         }
         mma_sync_point();
         if (*abort_flag) break;
@@ -606,6 +628,7 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
                         mma_bf16(tmem + tS, desc_mn(sb + (part ? L::oLo : L::oB), kk, part ? kTile : L::kHiBlock),
                                  desc_mn(sb + L::oX, kk), idesc_bf16(128, P, true, true), 1);
             }
+            mma_commit(mma_bar);
         }
         uint4 xr[4];  // this thread's x, before its tile is filled again
         if (a.D)
@@ -615,11 +638,12 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
                                                          sw128_offset(row, ((cp & 63) >> 3) + i));
         mma_sync_point();
         if (*abort_flag) break;
-        if (tid == 0 && k + 1 < cn) {
+        if (tid == kIo && k + 1 < cn) {
             issue_bc(k + 1);
             issue_x(k + 1);
             ++n_bc;
             ++n_x;
+            prefetch(k + 2);
         }
         __syncwarp();
         {   // y = Y1 + e^{c_i} Y2 + D x: 64 bytes of a row a thread
@@ -644,12 +668,12 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
         tc_before_sync();
     }
     if (*abort_flag) {
-        if (tid == 0) {  // wait, bounded, for the last of each copy and for the products
+        if (tid == 0 && mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
+        if (tid == kIo) {  // wait, bounded, for the last of each copy (and, above, for the products)
             record_status(GDR_ERR_TIMEOUT);
             mbar_wait(bar_g, (uint32_t)((n_g - 1) & 1));
             mbar_wait(bar_bc, (uint32_t)((n_bc - 1) & 1));
             mbar_wait(bar_x, (uint32_t)((n_x - 1) & 1));
-            if (mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
         }
     } else if (LO && a.S_T && row < N) {
         float *dst = a.S_T + (size_t)bh * P * N;

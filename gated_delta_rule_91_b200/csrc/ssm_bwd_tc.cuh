@@ -39,11 +39,11 @@ struct SsmGradTc {
     static constexpr uint32_t kAlloc = oBar + 64 + 1024;
 };
 
-// Column sums of a 32 x 32 block held as v[column] per lane (row): v[0] ends as the sum of column `lane`.
+// Column sums of a 32 x 16 block held as v[column] per lane (row): v[0] ends as the sum of column lane & 15.
 __device__ __forceinline__ void ssm_column_sums(float *v) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
+    for (int s = 8; s > 0; s >>= 1) {
         const bool up = lane & s;
 #pragma unroll
         for (int k = 0; k < s; ++k) {
@@ -51,6 +51,7 @@ __device__ __forceinline__ void ssm_column_sums(float *v) {
             v[k] = keep + __shfl_xor_sync(0xffffffffu, send, s);
         }
     }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 __device__ __forceinline__ double ssm_warp_scan(double x) {  // inclusive
     const int lane = threadIdx.x & 31;
@@ -67,8 +68,8 @@ template <int P, int N>
 __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_dy,
-    const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_g, SsmArgs a, int splits, int per,
-    const float *__restrict__ gates, const __nv_bfloat16 *__restrict__ Sin,
+    const __grid_constant__ CUtensorMap tm_dx, const __grid_constant__ CUtensorMap tm_s,
+    const __grid_constant__ CUtensorMap tm_g, SsmArgs a, int splits, int per, const float *__restrict__ gates, const __nv_bfloat16 *__restrict__ Sin,
     const __nv_bfloat16 *__restrict__ Gout, float *__restrict__ dBp, float *__restrict__ dCp, float *__restrict__ part) {
     using L = SsmGradTc<P, N>;
     using namespace sm100;
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 !mbar_wait(bar_y, (uint32_t)(hh & 1)))
                 *abort_flag = 1;
         }
+        if (tid == kIo) bulk_wait_read_all();  // the last head's dx leaves through the buffer of M' and dK
         __syncthreads();
         if (*abort_flag) break;
         if (tid == kIo && hh + 1 < nh) issue_g(hh + 1);  // the other table was last read a head ago
@@ -205,83 +207,91 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         mma_sync_point();
         if (*abort_flag) break;
-        // ---- M' = L K and dK = L W Delta: rows i, 32 columns j; R = M' W stays for the sums below ----
-        float rr[32], rsum = 0.f;
+        // ---- M' = L K, dK = L W Delta, and the sums of R = M' W: rows i, 32 columns j, 16 at a time (with all 32 the
+        // kernel spilled, and beside its shared memory there is next to no L1 for that) ----
         {
             uint8_t *dm = sm + L::oM + (prt >> 1) * kTile, *dk = sm + L::oK + (prt >> 1) * kTile;
-            const int cc = (prt & 1) * 4;
+            float rsum = 0.f;
             if (prt > q) {
                 const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    *reinterpret_cast<uint4 *>(dm + sw128_offset(row, cc + i)) = zero;
-                    *reinterpret_cast<uint4 *>(dk + sw128_offset(row, cc + i)) = zero;
+                    *reinterpret_cast<uint4 *>(dm + sw128_offset(row, (prt & 1) * 4 + i)) = zero;
+                    *reinterpret_cast<uint4 *>(dk + sw128_offset(row, (prt & 1) * 4 + i)) = zero;
                 }
+                s_colp[q * 128 + prt * 32 + lane] = 0.f;
             } else {
-                float kv[32], wv[32];
-                const float4 *dt4 = reinterpret_cast<const float4 *>(s_dt + prt * 32);
-                tmem_ld32(tl + tK + prt * 32, kv);
-                tmem_ld32(tl + tT + prt * 32, wv);
-                if (prt < q) {
-                    const float rf = s_g[SsmGate::rowf + row];
-                    const float2 rf2 = make_float2(rf, rf);
-                    float2 sum2 = make_float2(0.f, 0.f);
-                    const float4 *col4 = reinterpret_cast<const float4 *>(s_g + SsmGate::col + (q - 1) * 96 + prt * 32);
+                const float rf = s_g[SsmGate::rowf + row], ci = s_g[SsmGate::hi + row], cl = s_g[SsmGate::lo + row];
+                float dg = 0.f, wd = 0.f;
+#pragma unroll 1
+                for (int hb = 0; hb < 2; ++hb) {
+                    const int j0 = prt * 32 + hb * 16;
+                    float kv[16], wv[16], rr[16];
+                    const float4 *dt4 = reinterpret_cast<const float4 *>(s_dt + j0);
+                    tmem_ld16x2(tl + tK + j0, kv, tl + tT + j0, wv);
+                    if (prt < q) {
+                        const float2 rf2 = make_float2(rf, rf);
+                        float2 sum2 = make_float2(0.f, 0.f);
+                        const float4 *col4 = reinterpret_cast<const float4 *>(s_g + SsmGate::col + (q - 1) * 96 + j0);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 c4 = col4[i], d4 = dt4[i];
-                        const float2 c2[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
-                        const float2 d2[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 c4 = col4[i], d4 = dt4[i];
+                            const float2 c2[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+                            const float2 d2[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int n = 4 * i + 2 * u;
-                            const float2 l = fmul2(rf2, c2[u]), w = make_float2(wv[n], wv[n + 1]);
-                            const float2 kk = fmul2(make_float2(kv[n], kv[n + 1]), l), r = fmul2(kk, w);
-                            const float2 dk2 = fmul2(w, fmul2(l, d2[u]));
-                            sum2 = ffma2(r, d2[u], sum2);
-                            kv[n] = kk.x;
-                            kv[n + 1] = kk.y;
-                            rr[n] = r.x;
-                            rr[n + 1] = r.y;
-                            wv[n] = dk2.x;
-                            wv[n + 1] = dk2.y;
-                        }
-                    }
-                    rsum = sum2.x + sum2.y;
-                } else {
-                    const float ci = s_g[SsmGate::hi + row], cl = s_g[SsmGate::lo + row];
-                    const float4 *hi4 = reinterpret_cast<const float4 *>(s_g + SsmGate::hi + prt * 32);
-                    const float4 *lo4 = reinterpret_cast<const float4 *>(s_g + SsmGate::lo + prt * 32);
-                    float dg = 0.f, wd = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 h4 = hi4[i], l4 = lo4[i], d4 = dt4[i];
-                        const float l[4] = {exp2f((ci - h4.x) + (cl - l4.x)), exp2f((ci - h4.y) + (cl - l4.y)),
-                                            exp2f((ci - h4.z) + (cl - l4.z)), exp2f((ci - h4.w) + (cl - l4.w))};
-                        const float d[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int n = 4 * i + u;
-                            const float w = wv[n], r = kv[n] * l[u] * w;
-                            if (n == lane) {
-                                dg = r;
-                                wd = w;
+                            for (int u = 0; u < 2; ++u) {
+                                const int n = 4 * i + 2 * u;
+                                const float2 l = fmul2(rf2, c2[u]), w = make_float2(wv[n], wv[n + 1]);
+                                const float2 kk = fmul2(make_float2(kv[n], kv[n + 1]), l), r = fmul2(kk, w);
+                                const float2 dk2 = fmul2(w, fmul2(l, d2[u]));
+                                sum2 = ffma2(r, d2[u], sum2);
+                                kv[n] = kk.x;
+                                kv[n + 1] = kk.y;
+                                rr[n] = r.x;
+                                rr[n + 1] = r.y;
+                                wv[n] = dk2.x;
+                                wv[n + 1] = dk2.y;
                             }
-                            kv[n] = n <= lane ? kv[n] * l[u] : 0.f;
-                            wv[n] = n <= lane ? w * (l[u] * d[u]) : 0.f;
-                            rr[n] = n < lane ? r : 0.f;
-                            rsum = fmaf(rr[n], d[u], rsum);
+                        }
+                        rsum += sum2.x + sum2.y;
+                    } else {
+                        const float4 *hi4 = reinterpret_cast<const float4 *>(s_g + SsmGate::hi + j0);
+                        const float4 *lo4 = reinterpret_cast<const float4 *>(s_g + SsmGate::lo + j0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 h4 = hi4[i], l4 = lo4[i], d4 = dt4[i];
+                            const float l[4] = {exp2f((ci - h4.x) + (cl - l4.x)), exp2f((ci - h4.y) + (cl - l4.y)),
+                                                exp2f((ci - h4.z) + (cl - l4.z)), exp2f((ci - h4.w) + (cl - l4.w))};
+                            const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int n = 4 * i + u, at = hb * 16 + n;  // column of the block; the row's is lane
+                                const float w = wv[n], r = kv[n] * l[u] * w;
+                                if (at == lane) {
+                                    dg = r;
+                                    wd = w;
+                                }
+                                kv[n] = at <= lane ? kv[n] * l[u] : 0.f;
+                                wv[n] = at <= lane ? w * (l[u] * d[u]) : 0.f;
+                                rr[n] = at < lane ? r : 0.f;
+                                rsum = fmaf(rr[n], d[u], rsum);
+                            }
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        st_bf16x8(dm + sw128_offset(row, (prt & 1) * 4 + hb * 2 + i), kv + 8 * i);
+                        st_bf16x8(dk + sw128_offset(row, (prt & 1) * 4 + hb * 2 + i), wv + 8 * i);
+                    }
+                    ssm_column_sums(rr);
+                    if (lane < 16) s_colp[q * 128 + j0 + lane] = rr[0];
+                }
+                if (prt == q) {
                     s_diag[row] = dg;
                     s_wd[row] = wd;
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    st_bf16x8(dm + sw128_offset(row, cc + i), kv + 8 * i);
-                    st_bf16x8(dk + sw128_offset(row, cc + i), wv + 8 * i);
-                }
             }
+            s_rowp[prt * 128 + row] = rsum;
         }
         fence_async_smem();
         tc_before_sync();
@@ -303,13 +313,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             mma_commit(mma_bar);
         }
         __syncwarp();
-        if (prt <= q) {  // the sums of R, beside the products
-            ssm_column_sums(rr);
-            s_colp[q * 128 + prt * 32 + lane] = rr[0];
-        } else {
-            s_colp[q * 128 + prt * 32 + lane] = 0.f;
-        }
-        s_rowp[prt * 128 + row] = rsum;
         mma_sync_point();
         if (*abort_flag) break;
         if (tid == kIo) issue_state(&tm_s, unit);  // over M' and dK
@@ -342,15 +345,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             mma_commit(mma_bar);
         }
         __syncwarp();
-        float st[kChunks][8];
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            float lo[8];
-            ld8s(sm + L::oHi + chunk_off(i), st[i]);
-            ld8s(sm + L::oLo + chunk_off(i), lo);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) st[i][e] += lo[e];
-        }
         mma_sync_point();
         if (*abort_flag) break;
         if (tid == kIo) {
@@ -360,20 +354,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         __syncwarp();
         {
             const float e = s_g[SsmGate::e + row];
-            const int c = prt * NW;
-            float dot = 0.f, t[NW], acc[NW];
-            tmem_ldw<NW>(tl + tT + c, t);
-            tmem_ldw<NW>(tl + tC + c, acc);
+            float dot = 0.f;
+#pragma unroll 1
+            for (int c = prt * NW; c < (prt + 1) * NW; c += 16) {
+                float t[16], acc[16];
+                tmem_ld16x2(tl + tT + c, t, tl + tC + c, acc);
 #pragma unroll
-            for (int i = 0; i < NW / 8; ++i) {
-                float v[8];
-                ld8s(sm + L::oC + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), v);
+                for (int i = 0; i < 2; ++i) {
+                    float v[8];
+                    ld8s(sm + L::oC + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), v);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) dot = fmaf(v[k], t[8 * i + k], dot);
+                    for (int k = 0; k < 8; ++k) dot = fmaf(v[k], t[8 * i + k], dot);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] = fmaf(e, t[i], acc[i]);
+                tmem_st16(tl + tC + c, acc);
             }
-#pragma unroll
-            for (int i = 0; i < NW; ++i) acc[i] = fmaf(e, t[i], acc[i]);
-            tmem_stw<NW>(tl + tC + c, acc);
             tmem_wait_st();
             s_syp[prt * 128 + row] = e * dot;
         }
@@ -393,14 +389,23 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         __syncwarp();
         {
-            float dot = 0.f;  // <G, S_in>, each from its two parts
+            float dot = 0.f;  // <G, S_in>, each from its two parts; S_in once more, from L2
+            const uint4 *src = reinterpret_cast<const uint4 *>(Sin + unit * 2 * P * N) + tid;
+            uint4 sh[kChunks], sl[kChunks];
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
-                float x[8], y[8];
+                sh[i] = src[i * kGradThreads];
+                sl[i] = src[i * kGradThreads + P * N / 8];
+            }
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                float x[8], y[8], v[8], w[8];
                 ld8s(sm + L::oHi + chunk_off(i), x);
                 ld8s(sm + L::oLo + chunk_off(i), y);
+                ld8s(reinterpret_cast<const uint8_t *>(&sh[i]), v);
+                ld8s(reinterpret_cast<const uint8_t *>(&sl[i]), w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dot = fmaf(x[e] + y[e], st[i][e], dot);
+                for (int e = 0; e < 8; ++e) dot = fmaf(x[e] + y[e], v[e] + w[e], dot);
             }
             dot = warp_sum(dot, 32);
             if (lane == 0) s_red[warp] = dot;
@@ -411,20 +416,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         __syncwarp();
         {
             const float el = s_g[SsmGate::el + row], w = el * s_dt[row];
-            const int c = prt * NW;
-            float dot = 0.f, t[NW], acc[NW];
-            tmem_ldw<NW>(tl + tT + c, t);
-            tmem_ldw<NW>(tl + tB + c, acc);
+            float dot = 0.f;
+#pragma unroll 1
+            for (int c = prt * NW; c < (prt + 1) * NW; c += 16) {
+                float t[16], acc[16];
+                tmem_ld16x2(tl + tT + c, t, tl + tB + c, acc);
 #pragma unroll
-            for (int i = 0; i < NW / 8; ++i) {
-                float v[8];
-                ld8s(sm + L::oB + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), v);
+                for (int i = 0; i < 2; ++i) {
+                    float v[8];
+                    ld8s(sm + L::oB + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), v);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) dot = fmaf(v[k], t[8 * i + k], dot);
+                    for (int k = 0; k < 8; ++k) dot = fmaf(v[k], t[8 * i + k], dot);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, t[i], acc[i]);
+                tmem_st16(tl + tB + c, acc);
             }
-#pragma unroll
-            for (int i = 0; i < NW; ++i) acc[i] = fmaf(w, t[i], acc[i]);
-            tmem_stw<NW>(tl + tB + c, acc);
             tmem_wait_st();
             s_gxp[prt * 128 + row] = el * dot;
         }
@@ -481,26 +488,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         mma_sync_point();
         if (*abort_flag) break;
-        // ---- dx: a thread's columns of its row ----
+        // ---- dx, over G_out ----
         {
             const float w = s_g[SsmGate::el + row] * s_dt[row];
             const int c = prt * PW;
             float t[PW];
             tmem_ldw<PW>(tl + tT + c, t);
-            if (row < valid) {
-                uint8_t *dst = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(a.dx) +
-                                                           (((size_t)b * a.T + t0 + row) * a.H + h) * P + c);
 #pragma unroll
-                for (int i = 0; i < PW / 8; ++i) {
-                    float v[8];
+            for (int i = 0; i < PW; ++i) t[i] = fmaf(w, t[i], dxi[i]);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = fmaf(w, t[8 * i + k], dxi[8 * i + k]);
-                    st_bf16x8(dst + 16 * i, v);
-                }
-            }
+            for (int i = 0; i < PW / 8; ++i)
+                st_bf16x8(sm + L::oR + (uint32_t)(c >> 6) * kTile + sw128_offset(row, ((c & 63) >> 3) + i), t + 8 * i);
         }
+        fence_async_smem();
         tc_before_sync();
         __syncthreads();
+        if (tid == kIo) {
+            for (int i = 0; i < P / 64; ++i) tma_store_4d(&tm_dx, sm + L::oR + i * kTile, i * 64, h, t0, b);
+            bulk_commit();
+        }
+        __syncwarp();
         if (tid < 3) part[tid * units + unit] = (float)(s_tot[tid] + s_tot[3 + tid] + s_tot[6 + tid] + s_tot[9 + tid]);
     }
     if (*abort_flag) {
@@ -512,6 +519,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             mbar_wait(bar_y, (uint32_t)((n_y - 1) & 1));
             mbar_wait(bar_g, (uint32_t)((n_g - 1) & 1));
             if (n_s > 0) mbar_wait(bar_s, (uint32_t)((n_s - 1) & 1));
+            bulk_wait_all();
         }
     } else {
         tc_after_sync();
@@ -534,6 +542,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             }
         }
     }
+    if (tid == kIo) bulk_wait_all();
     tc_before_sync();
     __syncthreads();
     if (warp == 0) {
@@ -615,9 +624,10 @@ cudaError_t ssm_tc_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     float *dBp = reinterpret_cast<float *>(base + w.dBp), *dCp = reinterpret_cast<float *>(base + w.dCp);
     const size_t units = (size_t)a.B * nch * a.H;
     float *gates = reinterpret_cast<float *>(base + w.gates);
-    CUtensorMap mx, mb, mc, my, ms, mg;
+    CUtensorMap mx, mb, mc, my, mdx, ms, mg;
     if (!ssm_token_map(&mx, a.x, a.B, a.T, a.H, P, a.ldx) || !ssm_token_map(&mb, a.Bm, a.B, a.T, a.G, N, a.ldb) ||
         !ssm_token_map(&mc, a.Cm, a.B, a.T, a.G, N, a.ldc) || !ssm_token_map(&my, a.dy, a.B, a.T, a.H, P, a.H * P) ||
+        !ssm_token_map(&mdx, a.dx, a.B, a.T, a.H, P, a.H * P) ||
         !ssm_state_map(&ms, st, units, P, N) || !ssm_state_map(&mg, g, units, P, N))
         return cudaErrorInvalidValue;
     cudaError_t e = ssm_launch_gates(a, gates, s);
@@ -635,7 +645,7 @@ cudaError_t ssm_tc_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     const int per = (a.H / a.G + w.splits - 1) / w.splits;
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_grad_kernel<P, N>, dim3((unsigned)((size_t)a.B * nch * a.G * w.splits)), kGradThreads,
-                       (size_t)SsmGradTc<P, N>::kAlloc, s, mx, mb, mc, my, ms, mg, a, w.splits, per,
+                       (size_t)SsmGradTc<P, N>::kAlloc, s, mx, mb, mc, my, mdx, ms, mg, a, w.splits, per,
                        (const float *)gates, (const __nv_bfloat16 *)st, (const __nv_bfloat16 *)g, dBp, dCp, part);
     if (e != cudaSuccess) return e;
     if (w.splits > 1) {

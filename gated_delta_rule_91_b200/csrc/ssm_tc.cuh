@@ -95,8 +95,9 @@ struct SsmGate {
     static constexpr int col = 768;                       // [I-1][96]: 2^{r_I - c_j} of the blocks I = 1..3, j < 32 I
     static constexpr int last = 1056, elast = 1058;       // c_last (a double) and 2^{c_last}
     static constexpr int A = 1059, D = 1060;              // the head's (D: 0 without one)
-    static constexpr int sig = 1072, stride = 1200;       // d softplus / dz
-    static constexpr uint32_t kFwdBytes = sig * 4, kBytes = stride * 4;
+    static constexpr int misc = 1056, sig = 1072;         // (the last five: one copy of 64 bytes); d softplus / dz
+    static constexpr int w = 1200, stride = 1328;         // dt el
+    static constexpr uint32_t kFwdBytes = sig * 4, kBytes = w * 4;
 };
 // With c the sums in log2 units: e = 2^c, rowf = 2^{c - r} (r: c at the end of the block of 32 before the token's), el =
 // 2^{c_last - c}, and c in two parts (differences of nearby tokens are then exact to fp32 however far the sum has run).
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(128) ssm_gate_kernel(SsmArgs a, float *__restr
     out[SsmGate::el + t] = exp2f((float)(last - c));
     out[SsmGate::hi + t] = hi;
     out[SsmGate::lo + t] = (float)(c - (double)hi);
+    out[SsmGate::w + t] = d * exp2f((float)(last - c));
     out[SsmGate::sig + t] = a.softplus ? 1.f / (1.f + expf(-z)) : 1.f;
     for (int I = warp + 1; I < 4; ++I) {
         r += s_w[I - 1];
@@ -168,8 +170,9 @@ struct SsmWalkTc {
     static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile, kStage = XB + 2 * BB;
     static constexpr uint32_t oX = 0, oHi = XB, oLo = XB + BB, oZero = 2 * kStage;
     static constexpr uint32_t kSBlock = N * 128, SB = P / 64 * kSBlock;  // a state part as a tile: N rows
-    static constexpr uint32_t oGate = oZero + (N == 64 ? kTile : 0);     // two tables
-    static constexpr uint32_t oCtl = oGate + 2 * SsmGate::kFwdBytes;
+    static constexpr uint32_t oOut = oZero + (N == 64 ? kTile : 0);      // a state's second part on its way out
+    static constexpr uint32_t kGate = 128 * 4 + 64;                      // the rows' weights and the decay
+    static constexpr uint32_t oGate = oOut + SB, oCtl = oGate + 2 * kGate;
     static constexpr uint32_t kAlloc = oCtl + 96 + 1024;
 };
 
@@ -182,7 +185,6 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     using L = SsmWalkTc<P, N>;
     using namespace sm100;
     constexpr int PW = L::PW;
-    constexpr bool kBoth = P == 64;  // both parts of a state fit a stage's second-part buffer
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
@@ -222,9 +224,11 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             tma_load_4d(st + L::oHi + i * kTile, rev ? &tm_c : &tm_b, tma_bar + (k & 1), i * 64, g, chunk(k) * kTcQ, b);
     };
     auto issue_g = [&](int k) {
-        mbar_expect_tx(bar_g + (k & 1), SsmGate::kFwdBytes);
-        bulk_load_g2s(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes,
-                      gates + (((size_t)b * nch + chunk(k)) * a.H + h) * SsmGate::stride, SsmGate::kFwdBytes, bar_g + (k & 1));
+        const float *src = gates + (((size_t)b * nch + chunk(k)) * a.H + h) * SsmGate::stride;
+        uint8_t *dst = sm + L::oGate + (k & 1) * L::kGate;
+        mbar_expect_tx(bar_g + (k & 1), L::kGate);
+        bulk_load_g2s(dst, src + (rev ? SsmGate::e : SsmGate::w), 512, bar_g + (k & 1));
+        bulk_load_g2s(dst + 512, src + SsmGate::misc, 64, bar_g + (k & 1));
     };
     auto prefetch = [&](int k) {  // two stages leave less than a load's latency
         if (k >= cn) return;
@@ -247,10 +251,9 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             *abort_flag = 1;
             return;
         }
-        const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes);
         uint8_t *st = sm + (k & 1) * L::kStage;
         const int r = tid & 127;
-        const float w = rev ? s_g[SsmGate::e + r] : s_g[SsmGate::dt + r] * s_g[SsmGate::el + r];
+        const float w = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * L::kGate)[r];
         constexpr int CH = N / 32;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
@@ -285,8 +288,10 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     int k = 0;
 #pragma unroll 1
     for (; k < cn && !*abort_flag; ++k) {
-        const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes);
-        uint8_t *free_lo = sm + ((k + 1) & 1) * L::kStage + L::oLo;  // last read by the products of the chunk before
+        const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * L::kGate) + 128 - SsmGate::misc;
+        // A state leaves through the other stage's second-part buffer (last read by the products of the chunk before)
+        // and a buffer of its own.
+        uint8_t *out_hi = sm + ((k + 1) & 1) * L::kStage + L::oLo, *out_lo = sm + L::oOut;
         const float el = s_g[SsmGate::elast];
         const bool update = keep || k + 1 < cn;
         edge += *reinterpret_cast<const double *>(s_g + SsmGate::last);
@@ -296,19 +301,14 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             prefetch(k + 3);
         }
         __syncwarp();
-        float lo[PW];
         if (row < N) {
             tmem_ldw<PW>(tl, v);
-            if (OUT) {
-#pragma unroll
-                for (int i = 0; i < PW; ++i) lo[i] = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
+            if (OUT)
 #pragma unroll
                 for (int i = 0; i < PW / 8; ++i) {
                     const uint32_t off = (uint32_t)(cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i);
-                    st_bf16x8(free_lo + off, v + 8 * i);
-                    if (kBoth) st_bf16x8(free_lo + L::SB + off, lo + 8 * i);
+                    st_split8(out_hi + off, out_lo + off, v + 8 * i);
                 }
-            }
 #pragma unroll
             for (int i = 0; i < PW; ++i) v[i] *= el;
             tmem_stw<PW>(tl, v);
@@ -319,9 +319,9 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         __syncthreads();
         const int unit = (int)(((size_t)b * nch + chunk(k)) * a.H + h);
         if (OUT && tid == kIo) {
-            for (int pt = 0; pt < (kBoth ? 2 : 1); ++pt)
+            for (int pt = 0; pt < 2; ++pt)
                 for (int i = 0; i < P / 64; ++i)
-                    tma_store_4d(rev ? &tm_g : &tm_s, free_lo + pt * L::SB + i * L::kSBlock, i * 64, 0, pt, unit);
+                    tma_store_4d(rev ? &tm_g : &tm_s, (pt ? out_lo : out_hi) + i * L::kSBlock, i * 64, 0, pt, unit);
             bulk_commit();
         }
         if (tid == 0 && update) {
@@ -342,21 +342,6 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         if (OUT) {
             if (tid == kIo) bulk_wait_read_all();
             __syncthreads();
-            if (!kBoth) {
-                if (row < N)
-#pragma unroll
-                    for (int i = 0; i < PW / 8; ++i)
-                        st_bf16x8(free_lo + (uint32_t)(cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i), lo + 8 * i);
-                fence_async_smem();
-                __syncthreads();
-                if (tid == kIo) {
-                    for (int i = 0; i < P / 64; ++i)
-                        tma_store_4d(rev ? &tm_g : &tm_s, free_lo + i * L::kSBlock, i * 64, 0, 1, unit);
-                    bulk_commit();
-                    bulk_wait_read_all();
-                }
-                __syncthreads();
-            }
         }
         if (k + 1 < cn) convert(k + 1);
         fence_async_smem();
@@ -409,7 +394,7 @@ struct SsmYTc {
     static constexpr uint32_t oX = 0, oB = XB, oLo = oB + BB, oZero = oLo + (LO ? BB : 0);
     static constexpr uint32_t kHiBlock = N == 64 ? (LO ? 2 : 1) * kTile : kTile;
     static constexpr uint32_t oC = oZero + (N == 64 ? kTile : 0);  // C, then the decayed scores
-    static constexpr uint32_t kSBlock = N * 128;                   // S^T: N rows of 64 columns p
+    static constexpr uint32_t kSBlock = kTile;                     // S^T: N rows of 64 columns p; then y's tile
     static constexpr uint32_t oS = oC + 2 * kTile;
     static constexpr uint32_t oGate = oS + P / 64 * kSBlock;       // two tables
     static constexpr uint32_t oBar = oGate + 2 * SsmGate::kFwdBytes;
@@ -420,8 +405,8 @@ struct SsmYTc {
 template <int P, int N, bool LO>
 __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(
     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
-    const __grid_constant__ CUtensorMap tm_c, SsmArgs a, int m, const float *__restrict__ gates,
-    const float *__restrict__ states) {
+    const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y, SsmArgs a, int m,
+    const float *__restrict__ gates, const float *__restrict__ states) {
     using L = SsmYTc<P, N, LO>;
     using namespace sm100;
     extern __shared__ uint8_t smem_raw[];
@@ -514,9 +499,8 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
 #pragma unroll 1
     for (int k = 0; k < cn; ++k) {
         const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * SsmGate::kFwdBytes);
-        if (tid == 0) {
-            if (!mbar_wait(bar_g, (uint32_t)(k & 1))) *abort_flag = 1;
-        }
+        if (tid == 0 && !mbar_wait(bar_g, (uint32_t)(k & 1))) *abort_flag = 1;
+        if (tid == kIo) bulk_wait_read_all();  // y of the chunk before leaves through S's tile
         __syncthreads();
         if (*abort_flag) break;
         if (tid == kIo && k + 1 < cn) {  // the other table was last read a chunk ago
@@ -646,13 +630,12 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
             prefetch(k + 2);
         }
         __syncwarp();
-        {   // y = Y1 + e^{c_i} Y2 + D x: 64 bytes of a row a thread
+        {   // y = Y1 + e^{c_i} Y2 + D x, over S's tile (straight from registers, 64 bytes of 32 rows a warp, the
+            // stores alone took 2000 of a chunk's 9500 cycles)
             const float e = s_g[SsmGate::e + row];
-            const int t = (c0 + k) * kTcQ + row;
             float y1[32], y2[32];
             tmem_ld32(tl + tK + cp, y1);
             tmem_ld32(tl + tY2 + cp, y2);
-            uint8_t *dst = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(a.y) + (((size_t)b * a.T + t) * a.H + h) * P + cp);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float x[8];
@@ -662,10 +645,17 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
                     const float y = fmaf(e, y2[8 * i + u], y1[8 * i + u]);
                     x[u] = a.D ? fmaf(D, x[u], y) : y;
                 }
-                if (t < a.T) st_bf16x8(dst + 16 * i, x);
+                st_bf16x8(sm + L::oS + (uint32_t)(cp >> 6) * kTile + sw128_offset(row, ((cp & 63) >> 3) + i), x);
             }
         }
+        fence_async_smem();
         tc_before_sync();
+        __syncthreads();
+        if (tid == kIo) {
+            for (int i = 0; i < P / 64; ++i) tma_store_4d(&tm_y, sm + L::oS + i * kTile, i * 64, h, (c0 + k) * kTcQ, b);
+            bulk_commit();
+        }
+        __syncwarp();
     }
     if (*abort_flag) {
         if (tid == 0 && mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
@@ -674,6 +664,7 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
             mbar_wait(bar_g, (uint32_t)((n_g - 1) & 1));
             mbar_wait(bar_bc, (uint32_t)((n_bc - 1) & 1));
             mbar_wait(bar_x, (uint32_t)((n_x - 1) & 1));
+            bulk_wait_all();
         }
     } else if (LO && a.S_T && row < N) {
         float *dst = a.S_T + (size_t)bh * P * N;
@@ -682,6 +673,7 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
 #pragma unroll
         for (int i = 0; i < 32; ++i) dst[(size_t)(cp + i) * N + row] = v[i];
     }
+    if (tid == kIo) bulk_wait_all();
     tc_before_sync();
     __syncthreads();
     if (warp == 0) {
@@ -726,7 +718,7 @@ struct SsmTcFwdWs {
     size_t gates, st, dec, total;
 };
 inline size_t ssm_gate_bytes(int B, int T, int H) {
-    return ssm_align((size_t)B * ((T + kTcQ - 1) / kTcQ) * H * SsmGate::kBytes);
+    return ssm_align((size_t)B * ((T + kTcQ - 1) / kTcQ) * H * SsmGate::stride * sizeof(float));
 }
 inline SsmTcFwdWs ssm_tc_fwd_ws(int B, int T, int H, int P, int N) {
     const int m = ssm_tc_chunks(B, T, H, P), nch = (T + kTcQ - 1) / kTcQ, R = (nch + m - 1) / m;
@@ -748,9 +740,9 @@ inline cudaError_t ssm_launch_gates(const SsmArgs &a, float *gates, cudaStream_t
 
 template <int P, int N>
 cudaError_t ssm_tc_fwd(const SsmArgs &a, void *ws, cudaStream_t s) {
-    CUtensorMap mx, mb, mc;
+    CUtensorMap mx, mb, mc, my;
     if (!ssm_token_map(&mx, a.x, a.B, a.T, a.H, P, a.ldx) || !ssm_token_map(&mb, a.Bm, a.B, a.T, a.G, N, a.ldb) ||
-        !ssm_token_map(&mc, a.Cm, a.B, a.T, a.G, N, a.ldc))
+        !ssm_token_map(&mc, a.Cm, a.B, a.T, a.G, N, a.ldc) || !ssm_token_map(&my, a.y, a.B, a.T, a.H, P, a.H * P))
         return cudaErrorInvalidValue;
     const int m = ssm_tc_chunks(a.B, a.T, a.H, P), nch = (a.T + kTcQ - 1) / kTcQ, R = (nch + m - 1) / m;
     const dim3 grid((unsigned)(a.B * a.H) * (unsigned)R);
@@ -760,7 +752,7 @@ cudaError_t ssm_tc_fwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (R == 1)
         return ssm_launch(ssm_tc_y_kernel<P, N, true>, grid, SsmYTc<P, N, true>::NT, (size_t)SsmYTc<P, N, true>::kAlloc, s, mx,
-                          mb, mc, a, m, (const float *)gates, (const float *)nullptr);
+                          mb, mc, my, a, m, (const float *)gates, (const float *)nullptr);
     float *st = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.st);
     float *dec = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.dec);
     e = ssm_launch(ssm_tc_walk_kernel<P, N, false>, grid, SsmWalkTc<P, N>::kThreads, (size_t)SsmWalkTc<P, N>::kAlloc, s, mx, mb,
@@ -768,7 +760,7 @@ cudaError_t ssm_tc_fwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, R, a.H, P * N, st, dec, a.S0, a.S_T, s);
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_y_kernel<P, N, false>, grid, SsmYTc<P, N, false>::NT, (size_t)SsmYTc<P, N, false>::kAlloc, s, mx,
-                       mb, mc, a, m, (const float *)gates, (const float *)st);
+                       mb, mc, my, a, m, (const float *)gates, (const float *)st);
     return e;
 }
 

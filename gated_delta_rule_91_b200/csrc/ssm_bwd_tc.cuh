@@ -345,6 +345,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             mma_commit(mma_bar);
         }
         __syncwarp();
+        uint4 sh[kChunks], sl[kChunks];  // this thread's part of S_in, for <G, S_in>
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            sh[i] = *reinterpret_cast<const uint4 *>(sm + L::oHi + chunk_off(i));
+            sl[i] = *reinterpret_cast<const uint4 *>(sm + L::oLo + chunk_off(i));
+        }
         mma_sync_point();
         if (*abort_flag) break;
         if (tid == kIo) {
@@ -389,14 +395,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         __syncwarp();
         {
-            float dot = 0.f;  // <G, S_in>, each from its two parts; S_in once more, from L2
-            const uint4 *src = reinterpret_cast<const uint4 *>(Sin + unit * 2 * P * N) + tid;
-            uint4 sh[kChunks], sl[kChunks];
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                sh[i] = src[i * kGradThreads];
-                sl[i] = src[i * kGradThreads + P * N / 8];
-            }
+            float dot = 0.f;  // <G, S_in>, each from its two parts
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 float x[8], y[8], v[8], w[8];

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(int nch, int H, int PN4, 
 // ---- 3. outputs ----------------------------------------------------------------------------
 template <int P, int N>
 struct SsmYSmem {
-    static constexpr int kOp = 128 * kSsmLdQ > kSsmQ * 132 ? 128 * kSsmLdQ : kSsmQ * 132;  // one operand, floats
+    static constexpr int kOp = (P > N ? P : N) * kSsmLdQ;  // one operand, floats: [P or N][68] or [64][P or N + 4]
     static constexpr int kBytes = (3 * kOp + kSsmQ * kSsmLdQ) * 4;
 };
 template <typename T, int P, int N>
@@ -299,14 +299,16 @@ __device__ __forceinline__ void ssm_token_grads(const SsmArgs &a, int b, int h, 
 
 template <int P, int N>
 struct SsmGradSmem {
-    static constexpr int kOp = 128 * kSsmLdQ > kSsmQ * 132 ? 128 * kSsmLdQ : kSsmQ * 132;
+    static constexpr int kOp = (P > N ? P : N) * kSsmLdQ;
     static constexpr int kQQ = kSsmQ * kSsmLdQ;
     static constexpr int kBytes = (4 * kOp + 3 * kQQ) * 4;
 };
 
-// dBh, dCh: this head's gradients [B,T,H,N] fp32 (summed over each group by ssm_group_sum_kernel).
+// dBh, dCh: this head's gradients [B,T,H,N] fp32 (summed over each group by ssm_group_sum_kernel).  roles = 2: a chunk's
+// dx is a block of its own beside the rest; where the chunks do not fill the SMs that is shorter (a chunk with P = 128,
+// N = 64 takes 63 us as one block).
 template <typename T, int P, int N>
-__global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, const float *__restrict__ Sin,
+__global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, int roles, const float *__restrict__ Sin,
                                                                     const float *__restrict__ Gout,
                                                                     float *__restrict__ dBh, float *__restrict__ dCh,
                                                                     float *__restrict__ part) {
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, c
     __shared__ float s_part[16][kSsmQ];
     __shared__ double s_c[kSsmQ], s_red[8];
     const int nch = (a.T + kSsmQ - 1) / kSsmQ;
-    const int ch = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int ch = blockIdx.x / roles, role = roles == 1 ? 2 : blockIdx.x % roles, h = blockIdx.y, b = blockIdx.z;
     const int g = h / (a.H / a.G), t0 = ch * kSsmQ, valid = min(kSsmQ, a.T - t0);
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const size_t tok = (size_t)b * a.T + t0;
@@ -377,8 +379,9 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, c
         for (int k = 0; k < 16; ++k) s += s_part[k][tid];
         s_colU[tid] = s;
     }
+    __syncthreads();  // M' and dK are read next, whichever part comes first
     const double clast = s_c[kSsmQ - 1];
-    {   // dC: e^{c_i} S^T dy_i, its product with C_i, then the chunk's own part
+    if (role != 1) {  // dC: e^{c_i} S^T dy_i, its product with C_i, then the chunk's own part
         float acc[4][N / 16] = {};
 #pragma unroll 1
         for (int pb = 0; pb < P / 64; ++pb) {
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, c
                         make_float4(acc[r][4 * cb], acc[r][4 * cb + 1], acc[r][4 * cb + 2], acc[r][4 * cb + 3]);
         __syncthreads();
     }
-    {   // dB
+    if (role != 1) {  // dB
         float acc[4][N / 16] = {};
 #pragma unroll 1
         for (int pb = 0; pb < P / 64; ++pb) {
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, c
                         make_float4(acc[r][4 * cb], acc[r][4 * cb + 1], acc[r][4 * cb + 2], acc[r][4 * cb + 3]);
         __syncthreads();
     }
-    {   // dx
+    if (role != 0) {  // dx
         float acc[4][P / 16] = {};
 #pragma unroll 1
         for (int half = 0; half < N / 64; ++half) {
@@ -489,6 +492,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, c
             }
         }
     }
+    if (role == 1) return;
     double dot = 0.0;  // e^{c_last} <G, S_in>
     for (int i = tid; i < P * N; i += kSsmThreads) dot += (double)S[i] * (double)G[i];
     for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
@@ -617,9 +621,13 @@ cudaError_t ssm_simt_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     if (e == cudaSuccess) e = ssm_launch(ssm_state_simt_kernel<T, P, N, true>, grid, kSsmThreads, sm, s, a, g, dec);
     if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, nch, a.H, P * N, st, dec, a.S0, nullptr, s);
     if (e == cudaSuccess) e = ssm_launch_scan(true, a.B, nch, a.H, P * N, g, dec, a.dS_T, a.dS0, s);
+    int dev = 0, sms = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int roles = 2LL * nch * a.H * a.B <= sms ? 2 : 1;
     if (e == cudaSuccess)
-        e = ssm_launch(ssm_grad_simt_kernel<T, P, N>, dim3(nch, a.H, a.B), kSsmThreads, (size_t)SsmGradSmem<P, N>::kBytes, s,
-                       a, (const float *)st, (const float *)g, dBh, dCh, part);
+        e = ssm_launch(ssm_grad_simt_kernel<T, P, N>, dim3(nch * roles, a.H, a.B), kSsmThreads,
+                       (size_t)SsmGradSmem<P, N>::kBytes, s, a, roles, (const float *)st, (const float *)g, dBh, dCh, part);
     if (e != cudaSuccess) return e;
     const long long total4 = (long long)a.B * a.T * a.G * (N / 4);
     ssm_group_sum_kernel<T><<<dim3((unsigned)((total4 + 255) / 256), 2), 256, 0, s>>>(

@@ -244,7 +244,9 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             prefetch(k + 2);
         }
     __syncwarp();
-    // every thread: the chunk's rows weighted in place, the second part beside them
+    // every thread: the chunk's rows weighted in place, the second part in registers until its buffer is free
+    constexpr int CH = N / 32;
+    uint4 second[CH];
     auto convert = [&](int k) {
         const uint32_t par = (uint32_t)(k >> 1) & 1;
         if (!mbar_wait(bar_g + (k & 1), par) || !mbar_wait(tma_bar + (k & 1), par)) {
@@ -254,16 +256,24 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         uint8_t *st = sm + (k & 1) * L::kStage;
         const int r = tid & 127;
         const float w = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * L::kGate)[r];
-        constexpr int CH = N / 32;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = (tid >> 7) * CH + i;
-            const uint32_t off = (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
+            uint8_t *p = st + L::oHi + (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
             float x[8];
-            ld8s(st + L::oHi + off, x);
+            ld8s(p, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= w;
-            st_split8(st + L::oHi + off, st + L::oLo + off, x);
+            st_split8(p, reinterpret_cast<uint8_t *>(&second[i]), x);
+        }
+    };
+    auto convert_second = [&](int k) {
+        uint8_t *st = sm + (k & 1) * L::kStage + L::oLo;
+        const int r = tid & 127;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = (tid >> 7) * CH + i;
+            *reinterpret_cast<uint4 *>(st + (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7)) = second[i];
         }
     };
     float v[PW];
@@ -279,6 +289,7 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         tmem_wait_st();
     }
     convert(0);
+    convert_second(0);
     fence_async_smem();
     tc_before_sync();
     __syncthreads();
@@ -339,11 +350,12 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             mma_commit(mma_bar);
         }
         __syncwarp();
+        if (k + 1 < cn) convert(k + 1);
         if (OUT) {
             if (tid == kIo) bulk_wait_read_all();
             __syncthreads();
         }
-        if (k + 1 < cn) convert(k + 1);
+        if (k + 1 < cn) convert_second(k + 1);
         fence_async_smem();
         if (tid == 0 && update) {
             mma_open = !mbar_wait(mma_bar, (uint32_t)(k & 1));

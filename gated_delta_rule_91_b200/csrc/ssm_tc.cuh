@@ -6,10 +6,10 @@
 //     K  = C B^T                      M = 128 (i)   N = 128 (j)  K = N
 //     Y2 = C S_in^T                   M = 128 (i)   N = P        K = N
 //     Y1 = (K * L Delta) X            M = 128 (i)   N = P        K = 128 (j)
-//     S  = e^{c_last} S + (w B)^T X   M = 128 (n)   N = P        K = 128 (j)
+//     S  = e^{c_last} S + (w B)^T X   M = 128 (n)   N = P        K = 128 (j)   (or B^T (w X))
 //     y  = Y1 + e^{c_i} Y2 + D x,     w_j = e^{c_last - c_j} Delta_j
 // Roundings to bf16: the decayed scores (K * L Delta), the entering state as
-// the operand of Y2, and w B.  The state itself stays fp32 in TMEM, and where
+// the operand of Y2, and w B or w X.  The state itself stays fp32 in TMEM, and where
 // it is an output w B is split into two bf16 parts (its rounding is then below
 // 2^-17), so that S_T is exact to fp32 sums.
 //
@@ -406,7 +406,7 @@ struct SsmYTc {
     static constexpr uint32_t oX = 0, oB = XB, oLo = oB + BB, oZero = oLo + (LO ? BB : 0);
     static constexpr uint32_t kHiBlock = N == 64 ? (LO ? 2 : 1) * kTile : kTile;
     static constexpr uint32_t oC = oZero + (N == 64 ? kTile : 0);  // C, then the decayed scores
-    static constexpr uint32_t kSBlock = kTile;                     // S^T: N rows of 64 columns p; then y's tile
+    static constexpr uint32_t kSBlock = kTile;                     // S^T: N rows of 64 columns p; then w X, then y
     static constexpr uint32_t oS = oC + 2 * kTile;
     static constexpr uint32_t oGate = oS + P / 64 * kSBlock;       // two tables
     static constexpr uint32_t oBar = oGate + 2 * SsmGate::kFwdBytes;
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
             tmem_st32(tl + tS + cp, v);
             tmem_wait_st();
         }
-        if (tid == 0 && !mbar_wait(bar_bc, (uint32_t)(k & 1))) *abort_flag = 1;
+        if (tid == 0 && (!mbar_wait(bar_bc, (uint32_t)(k & 1)) || !mbar_wait(bar_x, (uint32_t)(k & 1)))) *abort_flag = 1;
         fence_async_smem();
         tc_before_sync();
         __syncthreads();
@@ -565,14 +565,19 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
                 const float4 *dt4 = reinterpret_cast<const float4 *>(s_g + SsmGate::dt + J * 32);
                 tmem_ld32(tl + tK + J * 32, v);
                 if (J < q) {
+                    const float2 rf2 = make_float2(rf, rf);
                     const float4 *col4 = reinterpret_cast<const float4 *>(s_g + SsmGate::col + (q - 1) * 96 + J * 32);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float4 cc = col4[i], d = dt4[i];
-                        v[4 * i] *= rf * cc.x * d.x;
-                        v[4 * i + 1] *= rf * cc.y * d.y;
-                        v[4 * i + 2] *= rf * cc.z * d.z;
-                        v[4 * i + 3] *= rf * cc.w * d.w;
+                        const float2 lo = fmul2(make_float2(v[4 * i], v[4 * i + 1]),
+                                                fmul2(fmul2(rf2, make_float2(cc.x, cc.y)), make_float2(d.x, d.y)));
+                        const float2 hi = fmul2(make_float2(v[4 * i + 2], v[4 * i + 3]),
+                                                fmul2(fmul2(rf2, make_float2(cc.z, cc.w)), make_float2(d.z, d.w)));
+                        v[4 * i] = lo.x;
+                        v[4 * i + 1] = lo.y;
+                        v[4 * i + 2] = hi.x;
+                        v[4 * i + 3] = hi.y;
                     }
                 } else {
                     const float4 *hi4 = reinterpret_cast<const float4 *>(s_g + SsmGate::hi + J * 32);
@@ -590,27 +595,39 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
 #pragma unroll
             for (int i = 0; i < 4; ++i) st_bf16x8(dst + sw128_offset(row, (J & 1) * 4 + i), v + 8 * i);
         }
-        if (LO || k + 1 < cn) {  // w B in place (B's product is done), its second part beside it
+        {   // the state's own product: w B in place (B's product is done) with its second part beside it, or, where one
+            // bf16 part will do, w X over S's tile (its product is done), which is the smaller of the two
             const int r = tid & 127;
             const float w = s_g[SsmGate::dt + r] * s_g[SsmGate::el + r];
-            constexpr int CH = N / 8 / L::kParts;
+            if (LO) {
+                constexpr int CH = N / 8 / L::kParts;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = (tid >> 7) * CH + i;
-                uint8_t *p = sm + L::oB + (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
-                float v[8];
-                ld8s(p, v);
+                for (int i = 0; i < CH; ++i) {
+                    const int c = (tid >> 7) * CH + i;
+                    uint8_t *p = sm + L::oB + (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
+                    float v[8];
+                    ld8s(p, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= w;
-                if (LO) st_split8(p, p + L::BB, v);
-                else st_bf16x8(p, v);
+                    for (int e = 0; e < 8; ++e) v[e] *= w;
+                    st_split8(p, p + L::BB, v);
+                }
+            } else if (k + 1 < cn) {
+                constexpr int CH = P / 8 / L::kParts;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int c = (tid >> 7) * CH + i;
+                    const uint32_t off = (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
+                    float v[8];
+                    ld8s(sm + L::oX + off, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= w;
+                    st_bf16x8(sm + L::oS + off, v);
+                }
             }
         }
-        if (tid == 0 && !mbar_wait(bar_x, (uint32_t)(k & 1))) *abort_flag = 1;
         fence_async_smem();
         tc_before_sync();
         __syncthreads();
-        if (*abort_flag) break;
         if (tid == 0) {
             tc_after_sync();
 #pragma unroll
@@ -622,7 +639,7 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
                         mma_bf16(tmem + tS, desc_mn(sb + (part ? L::oLo : L::oB), kk, part ? kTile : L::kHiBlock),
-                                 desc_mn(sb + L::oX, kk), idesc_bf16(128, P, true, true), 1);
+                                 desc_mn(sb + (LO ? L::oX : L::oS), kk), idesc_bf16(128, P, true, true), 1);
             }
             mma_commit(mma_bar);
         }

@@ -157,18 +157,20 @@ inline bool ssm_state_map(CUtensorMap *map, const void *base, size_t units, int 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A CTA walks the chunks of one (b, h, segment), forwards (S <- e^{c_last} S + (w B)^T X) or, rev, backwards (G <-
-// e^{c_last} G + (e^c C)^T dY), the state in TMEM (lanes n, columns p, fp32), the weighted rows in two bf16 parts.
+// A CTA walks the chunks of one (b, h, segment), forwards (S <- e^{c_last} S + B^T (w X)) or, rev, backwards (G <-
+// e^{c_last} G + C^T (e^c dY)), the state in TMEM (lanes n, columns p, fp32), the weighted rows in two bf16 parts.
 // OUT: from the state that enters the segment, every chunk's entering state is written as two bf16 parts (out_S, out_G
 // through tm_s, tm_g), and dS0 at the end.  Otherwise: from zero, the segment's own sum goes to seg_S or seg_G
 // [b][seg][h][P][N] in fp32, and its decay to dec.
-// Two stages of operands: while a chunk's products run, the next chunk's rows are weighted (a chunk takes about 2500
-// cycles; with one stage and half the warps it took 4500, or 9400 where the states were stored row by row).
+// Two or three stages of operands: while a chunk's products run, the next chunk's rows are weighted (without states to
+// write a chunk takes about 3900 cycles at P = N = 128; with one stage and half the warps it took 4500, and 9400 with
+// states stored row by row against 5600 now).  What bounds it is the operands' way from L2: 64 KB a chunk and SM.
 template <int P, int N>
 struct SsmWalkTc {
     static constexpr int kThreads = 512, PW = P / 4;
-    static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile, kStage = XB + 2 * BB;
-    static constexpr uint32_t oX = 0, oHi = XB, oLo = XB + BB, oZero = 2 * kStage;
+    static constexpr int ST = P == 64 ? 3 : 2;                           // stages
+    static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile, kStage = 2 * XB + BB;
+    static constexpr uint32_t oX = 0, oLo = XB, oB = 2 * XB, oZero = ST * kStage;  // X, weighted in place; its second part
     static constexpr uint32_t kSBlock = N * 128, SB = P / 64 * kSBlock;  // a state part as a tile: N rows
     static constexpr uint32_t oOut = oZero + (N == 64 ? kTile : 0);      // a state's second part on its way out
     static constexpr uint32_t kGate = 128 * 4 + 64;                      // the rows' weights and the decay
@@ -188,8 +190,9 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
-    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(sm + L::oCtl), *bar_g = tma_bar + 2, *mma_bar = tma_bar + 4;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tma_bar + 5);
+    constexpr int ST = L::ST;
+    uint64_t *tma_bar = reinterpret_cast<uint64_t *>(sm + L::oCtl), *bar_g = tma_bar + ST, *mma_bar = bar_g + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = warp & 3, prt = warp >> 2, row = q * 32 + lane, cp = prt * PW;  // state row n, first column p
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     auto chunk = [&](int k) { return rev ? c0 + cn - 1 - k : c0 + k; };
 
     if (tid == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(tma_bar + i, 1);
+        for (int i = 0; i < ST + 3; ++i) mbar_init(tma_bar + i, 1);
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -216,12 +219,13 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + cp;
     constexpr int kIo = 384;  // the thread that issues copies; thread 0 issues products
     auto issue = [&](int k) {
-        uint8_t *st = sm + (k & 1) * L::kStage;
-        mbar_expect_tx(tma_bar + (k & 1), L::XB + L::BB);
+        uint8_t *st = sm + (k % ST) * L::kStage;
+        uint64_t *bar = tma_bar + k % ST;
+        mbar_expect_tx(bar, L::XB + L::BB);
         for (int i = 0; i < P / 64; ++i)
-            tma_load_4d(st + L::oX + i * kTile, rev ? &tm_dy : &tm_x, tma_bar + (k & 1), i * 64, h, chunk(k) * kTcQ, b);
+            tma_load_4d(st + L::oX + i * kTile, rev ? &tm_dy : &tm_x, bar, i * 64, h, chunk(k) * kTcQ, b);
         for (int i = 0; i < N / 64; ++i)
-            tma_load_4d(st + L::oHi + i * kTile, rev ? &tm_c : &tm_b, tma_bar + (k & 1), i * 64, g, chunk(k) * kTcQ, b);
+            tma_load_4d(st + L::oB + i * kTile, rev ? &tm_c : &tm_b, bar, i * 64, g, chunk(k) * kTcQ, b);
     };
     auto issue_g = [&](int k) {
         const float *src = gates + (((size_t)b * nch + chunk(k)) * a.H + h) * SsmGate::stride;
@@ -230,36 +234,38 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         bulk_load_g2s(dst, src + (rev ? SsmGate::e : SsmGate::w), 512, bar_g + (k & 1));
         bulk_load_g2s(dst + 512, src + SsmGate::misc, 64, bar_g + (k & 1));
     };
-    auto prefetch = [&](int k) {  // two stages leave less than a load's latency
+    auto prefetch = [&](int k) {  // two stages leave less than a load's latency from memory
         if (k >= cn) return;
         for (int i = 0; i < P / 64; ++i) tma_prefetch_4d(rev ? &tm_dy : &tm_x, i * 64, h, chunk(k) * kTcQ, b);
         for (int i = 0; i < N / 64; ++i) tma_prefetch_4d(rev ? &tm_c : &tm_b, i * 64, g, chunk(k) * kTcQ, b);
     };
     int n_t = 0, n_g = 0;  // issued, by that thread
     if (tid == kIo)
-        for (int k = 0; k < 2 && k < cn; ++k) {
-            issue_g(k);
+        for (int k = 0; k < ST && k < cn; ++k) {
+            if (k < 2) {
+                issue_g(k);
+                n_g = k + 1;
+            }
             issue(k);
-            n_t = n_g = k + 1;
-            prefetch(k + 2);
+            n_t = k + 1;
+            if (ST == 2) prefetch(k + 2);
         }
     __syncwarp();
     // every thread: the chunk's rows weighted in place, the second part in registers until its buffer is free
-    constexpr int CH = N / 32;
+    constexpr int CH = P / 32;
     uint4 second[CH];
     auto convert = [&](int k) {
-        const uint32_t par = (uint32_t)(k >> 1) & 1;
-        if (!mbar_wait(bar_g + (k & 1), par) || !mbar_wait(tma_bar + (k & 1), par)) {
+        if (!mbar_wait(bar_g + (k & 1), (uint32_t)(k >> 1) & 1) || !mbar_wait(tma_bar + k % ST, (uint32_t)(k / ST) & 1)) {
             *abort_flag = 1;
             return;
         }
-        uint8_t *st = sm + (k & 1) * L::kStage;
+        uint8_t *st = sm + (k % ST) * L::kStage + L::oX;
         const int r = tid & 127;
         const float w = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * L::kGate)[r];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = (tid >> 7) * CH + i;
-            uint8_t *p = st + L::oHi + (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
+            uint8_t *p = st + (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
             float x[8];
             ld8s(p, x);
 #pragma unroll
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         }
     };
     auto convert_second = [&](int k) {
-        uint8_t *st = sm + (k & 1) * L::kStage + L::oLo;
+        uint8_t *st = sm + (k % ST) * L::kStage + L::oLo;
         const int r = tid & 127;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
@@ -300,16 +306,16 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
 #pragma unroll 1
     for (; k < cn && !*abort_flag; ++k) {
         const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * L::kGate) + 128 - SsmGate::misc;
-        // A state leaves through the other stage's second-part buffer (last read by the products of the chunk before)
-        // and a buffer of its own.
-        uint8_t *out_hi = sm + ((k + 1) & 1) * L::kStage + L::oLo, *out_lo = sm + L::oOut;
+        // A state leaves through the second-part buffer of the stage of the chunk before (its products are done) and a
+        // buffer of its own.
+        uint8_t *out_hi = sm + ((k + ST - 1) % ST) * L::kStage + L::oLo, *out_lo = sm + L::oOut;
         const float el = s_g[SsmGate::elast];
         const bool update = keep || k + 1 < cn;
         edge += *reinterpret_cast<const double *>(s_g + SsmGate::last);
-        if (tid == kIo && k > 0 && k + 1 < cn) {
-            issue(k + 1);
-            n_t = k + 2;
-            prefetch(k + 3);
+        if (tid == kIo && k > 0 && k - 1 + ST < cn) {  // into the stage of the chunk before
+            issue(k - 1 + ST);
+            n_t = k + ST;
+            if (ST == 2) prefetch(k + 3);
         }
         __syncwarp();
         if (row < N) {
@@ -337,24 +343,20 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         }
         if (tid == 0 && update) {
             tc_after_sync();
-            const uint32_t st = sb + (k & 1) * L::kStage;
+            const uint32_t st = sb + (k % ST) * L::kStage, at = st + L::oB;
+            const uint32_t block = N == 64 ? sb + L::oZero - at : kTile;  // the second 64 lanes
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                const uint32_t at = st + (part ? L::oLo : L::oHi);
-                const uint32_t block = N == 64 ? sb + L::oZero - at : kTile;  // the second 64 lanes
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16(tmem, desc_mn(at, kk, block), desc_mn(st + L::oX, kk),
+                    mma_bf16(tmem, desc_mn(at, kk, block), desc_mn(st + (part ? L::oLo : L::oX), kk),
                              idesc_bf16(128, P, true, true), 1);
-            }
             mma_commit(mma_bar);
         }
         __syncwarp();
         if (k + 1 < cn) convert(k + 1);
-        if (OUT) {
-            if (tid == kIo) bulk_wait_read_all();
-            __syncthreads();
-        }
+        if (OUT && tid == kIo) bulk_wait_read_all();
+        if (OUT && ST == 2) __syncthreads();  // out_hi is where the next second part goes
         if (k + 1 < cn) convert_second(k + 1);
         fence_async_smem();
         if (tid == 0 && update) {
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     if (*abort_flag) {
         if (tid == kIo) {
             record_status(GDR_ERR_TIMEOUT);
-            for (int i = n_t > 1 ? n_t - 2 : 0; i < n_t; ++i) mbar_wait(tma_bar + (i & 1), (uint32_t)(i >> 1) & 1);
+            for (int i = n_t > ST ? n_t - ST : 0; i < n_t; ++i) mbar_wait(tma_bar + i % ST, (uint32_t)(i / ST) & 1);
             for (int i = n_g > 1 ? n_g - 2 : 0; i < n_g; ++i) mbar_wait(bar_g + (i & 1), (uint32_t)(i >> 1) & 1);
             if (OUT) bulk_wait_all();
         }

@@ -37,9 +37,16 @@ gdr_status check_ssm(const char *fn, int B, int T, int H, int G, int P, int N, g
     if (H % G != 0) return fail(GDR_ERR_INVALID_ARGUMENT, "%s: H=%d is not a multiple of G=%d", fn, H, G);
     if ((long long)B * T * H * (P > N ? P : N) >= (1LL << 31))
         return fail(GDR_ERR_UNSUPPORTED, "%s: B*T*H*max(P,N) exceeds 2^31-1", fn);
-    if ((long long)B * H * (P / 32) >= (1LL << 31) || (T > 1 && (B > 65535 || H > 65535)))
+    if ((long long)B * H * (P / 32) >= (1LL << 31))
         return fail(GDR_ERR_UNSUPPORTED, "%s: too many batches or heads (B=%d H=%d)", fn, B, H);
     return GDR_OK;
+}
+// The prompt's and the gradients' kernels take heads and batches as grid axes.
+gdr_status check_ssm_grid(const char *fn, int B, int T, int H, int G, int P, int N, gdr_dtype dt) {
+    gdr_status st = check_ssm(fn, B, T, H, G, P, N, dt);
+    if (st == GDR_OK && (B > 65535 || H > 65535))
+        return fail(GDR_ERR_UNSUPPORTED, "%s: B=%d H=%d (at most 65535 each)", fn, B, H);
+    return st;
 }
 
 // Token stride `ld` of `width` elements: 0 means dense; rows start on 16-byte boundaries.
@@ -98,7 +105,7 @@ gdr_status check_norm(const char *fn, long long R, int D, gdr_dtype dt, float ep
 extern "C" {
 
 size_t gdr_ssm_fwd_workspace_bytes(int B, int T, int H, int G, int P, int N, gdr_dtype dt) {
-    if (check_ssm("gdr_ssm_fwd_workspace_bytes", B, T, H, G, P, N, dt) != GDR_OK) return 0;
+    if (check_ssm_grid("gdr_ssm_fwd_workspace_bytes", B, T, H, G, P, N, dt) != GDR_OK) return 0;
     return ssm_uses_tc(dt) ? ssm_tc_fwd_ws(B, T, H, P, N).total : ssm_simt_ws(B, T, H, P, N).fwd_total;
 }
 
@@ -107,7 +114,7 @@ gdr_status gdr_ssm_fwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, i
                        const float *D, const float *delta_bias, const float *S0, void *y, float *S_T, void *workspace,
                        size_t workspace_bytes, gdr_stream_t stream) {
     const char *fn = "gdr_ssm_fwd";
-    gdr_status st = check_ssm(fn, B, T, H, G, P, N, dt);
+    gdr_status st = check_ssm_grid(fn, B, T, H, G, P, N, dt);
     if (st == GDR_OK) st = check_stride(fn, "ldx", &ldx, H * P, dt);
     if (st == GDR_OK) st = check_stride(fn, "ldb", &ldb, G * N, dt);
     if (st == GDR_OK) st = check_stride(fn, "ldc", &ldc, G * N, dt);
@@ -140,7 +147,7 @@ gdr_status gdr_ssm_fwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, i
 }
 
 size_t gdr_ssm_bwd_workspace_bytes(int B, int T, int H, int G, int P, int N, gdr_dtype dt) {
-    if (check_ssm("gdr_ssm_bwd_workspace_bytes", B, T, H, G, P, N, dt) != GDR_OK) return 0;
+    if (check_ssm_grid("gdr_ssm_bwd_workspace_bytes", B, T, H, G, P, N, dt) != GDR_OK) return 0;
     return ssm_uses_tc(dt) ? ssm_tc_bwd_ws(B, T, H, G, P, N).total : ssm_simt_ws(B, T, H, P, N).bwd_total;
 }
 
@@ -150,7 +157,7 @@ gdr_status gdr_ssm_bwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, i
                        void *dx, float *ddelta, float *dA, void *dB, void *dC, float *dD, float *ddelta_bias, float *dS0,
                        void *workspace, size_t workspace_bytes, gdr_stream_t stream) {
     const char *fn = "gdr_ssm_bwd";
-    gdr_status st = check_ssm(fn, B, T, H, G, P, N, dt);
+    gdr_status st = check_ssm_grid(fn, B, T, H, G, P, N, dt);
     if (st == GDR_OK) st = check_stride(fn, "ldx", &ldx, H * P, dt);
     if (st == GDR_OK) st = check_stride(fn, "ldb", &ldb, G * N, dt);
     if (st == GDR_OK) st = check_stride(fn, "ldc", &ldc, G * N, dt);

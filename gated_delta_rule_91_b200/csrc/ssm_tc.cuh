@@ -727,16 +727,19 @@ inline int ssm_sm_count() {
     return n;
 }
 
-// Chunks per segment: the fewest rounds of chunks over the SMs' places, where an extra segment costs its state's
-// traffic (about a fifth of a chunk's time in each of the launches).
+// Chunks per segment.  In units of a chunk of the output kernel: whole rounds of CTAs over the SMs, where two CTAs of P =
+// 64 on an SM take 1.75 of one's time; a cut costs the walk over the segments first (about half of that) and two
+// launches.  Measured: B=4 T=4096 H=16 P=N=128, 2 segments 145 us (3: over 164); B=1 T=4096, 8 segments 51 us (16: 56);
+// B=8 T=2048 H=16 P=64, uncut 90 us (2 segments: 102); B=1 T=65536 P=64, 37 segments 307 us (32: 330).
 inline int ssm_tc_chunks(int B, int T, int H, int P) {
-    const int nch = (T + kTcQ - 1) / kTcQ, places = ssm_sm_count() * (P == 64 ? 2 : 1);
+    const int nch = (T + kTcQ - 1) / kTcQ, sms = ssm_sm_count();
     double best = 1e30;
     int at = nch;
     for (int m = nch; m >= 1; m = m > 64 ? m * 3 / 4 : m - 1) {
         const int R = (nch + m - 1) / m;
-        const double rounds = (double)(((long long)B * H * R + places - 1) / places);
-        const double cost = R == 1 ? rounds * m : rounds * (1.4 * m + 1.0) + 2.0;
+        const long long n = (long long)B * H * R, rounds = (n + sms - 1) / sms;
+        const double y = P == 64 && R > 1 && n > sms ? (double)((n + 2 * sms - 1) / (2 * sms)) * 1.75 : (double)rounds;
+        const double cost = R == 1 ? y * 1.1 * m : y * m + (double)rounds * (0.5 * m + 1.0) + 2.0;
         if (cost < best * 0.999) {
             best = cost;
             at = m;

@@ -420,9 +420,10 @@ GDR_API gdr_status gdr_seg_fixup(int B, int T, int H, int dk, int dv, gdr_dtype 
  *   it is: a batch of unequal prompts is padded with such tokens (on the left
  *   if the convolution's window goes on from its end).  Inputs are finite
  *   (delta may be -inf); a value that is not spoils the outputs of its chunk of
- *   128 tokens and of what follows.
+ *   128 tokens and of what follows.  A Delta_t <= 0 is what the chunk form is
+ *   made for; a state that grows by more than 2^127 inside a chunk overflows.
  *   Supported: P, N in {64, 128}; H a multiple of G; B*T*H*max(P,N) < 2^31;
- *   B, H <= 65535 where T > 1.  workspace: gdr_ssm_fwd_workspace_bytes(...)
+ *   B, H <= 65535.  workspace: gdr_ssm_fwd_workspace_bytes(...)
  *   bytes; NULL or short -> GDR_ERR_WORKSPACE.  Repeated calls give the same bits.
  */
 GDR_API gdr_status gdr_ssm_fwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, int softplus,

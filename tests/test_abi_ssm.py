@@ -42,7 +42,7 @@ def test_scan_refusals(fn, kw, status):
 
 @pytest.mark.parametrize("fn,kw,status", [
     ("gdr_ssm_fwd", dict(S0=FAKE + 8), BAD), ("gdr_ssm_fwd", dict(S_T=FAKE + 8), BAD), ("gdr_ssm_fwd", dict(T=0), BAD),
-    ("gdr_ssm_fwd", dict(B=70000, T=2, H=2), UNS), ("gdr_ssm_bwd", dict(dS_T=FAKE + 4), BAD), ("gdr_ssm_bwd", dict(dx=None), BAD),
+    ("gdr_ssm_fwd", dict(B=70000, T=1, H=2), UNS), ("gdr_ssm_bwd", dict(B=2, T=2, H=70000), UNS), ("gdr_ssm_bwd", dict(dS_T=FAKE + 4), BAD), ("gdr_ssm_bwd", dict(dx=None), BAD),
     ("gdr_ssm_bwd", dict(dA=None), BAD), ("gdr_ssm_bwd", dict(ws=None), WS), ("gdr_ssm_bwd", dict(nws=1000), WS),
     ("gdr_ssm_bwd", dict(ws=FAKE + 8), BAD), ("gdr_ssm_step", dict(S=None), BAD), ("gdr_ssm_step", dict(S=FAKE + 4), BAD)])
 def test_scan_refusals_of_its_own(fn, kw, status):

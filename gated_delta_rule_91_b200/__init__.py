@@ -384,16 +384,21 @@ def gdr_seg_fixup(qt, S_in, o):
     return o
 
 
-def _like(name, t, shape, dtype, device):
-    """`t` (None passes) as a dense operand of this shape, type and device; returns its address."""
-    if t is None:
-        return None
+def _mismatch(name, t, shape, dtype, device):
+    """Raises what is wrong with an operand."""
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device or not t.is_cuda:
-        raise ValueError("%s must be on the CUDA device of the other tensors (%s), got %s" % (name, device, t.device))
+    raise ValueError("%s must be on the CUDA device of the other tensors (%s), got %s" % (name, device, t.device))
+
+
+def _like(name, t, shape, dtype, device):
+    """`t` (None passes) as a dense operand of this shape, type and (CUDA) device; returns its address."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _mismatch(name, t, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
@@ -401,13 +406,11 @@ def _like(name, t, shape, dtype, device):
 
 def _rows(name, t, shape, lead, dtype, device):
     """`t` as rows of a wider buffer: the axes from `lead` on are a dense row, and the rows of the leading axes are
-    one stride apart.  Returns (address, stride in elements)."""
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device or not t.is_cuda:
-        raise ValueError("%s must be on the CUDA device of the other tensors (%s), got %s" % (name, device, t.device))
+    one stride apart.  Returns (address, stride in elements; 0: dense)."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _mismatch(name, t, shape, dtype, device)
+    if t.is_contiguous():
+        return t.data_ptr(), 0
     strides = t.stride()
     width = 1
     for i in range(len(shape) - 1, lead - 1, -1):
@@ -424,7 +427,7 @@ def _rows(name, t, shape, lead, dtype, device):
             elif strides[i] != rows * ld:
                 raise ValueError("%s: the rows of all batches must be one stride apart" % name)
             rows *= shape[i]
-    return t.data_ptr(), ld or width
+    return t.data_ptr(), ld
 
 
 def _launch(device, fn, *args):

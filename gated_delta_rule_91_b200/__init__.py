@@ -482,7 +482,7 @@ def gdr_ssm_fwd(x, delta, A, Bm, Cm, D=None, delta_bias=None, S0=None, *, softpl
     (B, T), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 2)
     y = x.new_empty((B, T, H, P)) if y is None else y
     if S_T is None and return_state:
-        S_T = torch.empty(B, H, P, N, dtype=torch.float32, device=dev)
+        S_T = delta.new_empty((B, H, P, N))
     f = torch.float32
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_ssm_fwd_workspace_bytes(B, T, H, G, P, N, dt), dev, workspace)
@@ -498,10 +498,11 @@ def gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, dy, dS_T=None, *, softpl
     None without D and delta_bias."""
     (B, T), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 2)
     f = torch.float32
-    e = lambda *shape, dtype=f: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
-    out = dict(dx=e(B, T, H, P, dtype=x.dtype), ddelta=e(B, T, H), dA=e(H), dB=e(B, T, G, N, dtype=x.dtype),
-               dC=e(B, T, G, N, dtype=x.dtype), dD=None if D is None else e(H),
-               ddelta_bias=None if delta_bias is None else e(H), dS0=e(B, H, P, N) if want_dS0 else None)
+    like = torch.empty_like  # the dense ones
+    out = dict(dx=x.new_empty((B, T, H, P)), ddelta=like(delta), dA=like(A), dB=x.new_empty((B, T, G, N)),
+               dC=x.new_empty((B, T, G, N)), dD=None if D is None else like(D),
+               ddelta_bias=None if delta_bias is None else like(delta_bias),
+               dS0=delta.new_empty((B, H, P, N)) if want_dS0 else None)
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_ssm_bwd_workspace_bytes(B, T, H, G, P, N, dt), dev, workspace)
     _launch(dev, L.gdr_ssm_bwd, B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev),

@@ -55,22 +55,6 @@ template <> struct ConvVec<__nv_bfloat16, 4> {
         *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(h);
     }
 };
-template <> struct ConvVec<float, 2> {
-    static __device__ __forceinline__ void ld(const float *p, float *v) {
-        const float2 u = *reinterpret_cast<const float2 *>(p);
-        v[0] = u.x; v[1] = u.y;
-    }
-    static __device__ __forceinline__ void st(float *p, const float *v) { *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]); }
-};
-template <> struct ConvVec<__nv_bfloat16, 2> {
-    static __device__ __forceinline__ void ld(const __nv_bfloat16 *p, float *v) {
-        const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
-        v[0] = u.x; v[1] = u.y;
-    }
-    static __device__ __forceinline__ void st(__nv_bfloat16 *p, const float *v) {
-        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[1]);
-    }
-};
 template <typename T> struct ConvVec<T, 1> {
     static __device__ __forceinline__ void ld(const T *p, float *v) { v[0] = to_f32(*p); }
     static __device__ __forceinline__ void st(T *p, const float *v) { *p = from_f32<T>(v[0]); }
@@ -88,12 +72,6 @@ template <> struct RowRaw<__nv_bfloat16, 4> {
 };
 template <> struct RowRaw<float, 4> {
     float4 e;
-};
-template <> struct RowRaw<float, 2> {
-    float2 e;
-};
-template <> struct RowRaw<__nv_bfloat16, 2> {
-    uint32_t e;
 };
 template <typename T, int V>
 __device__ __forceinline__ void raw_values(const RowRaw<T, V> &r, float *v) {
@@ -225,7 +203,7 @@ struct ConvStage {
 
 // Forward: a warp is 32 V channels of one run.
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(256, K <= 4 ? 3 : 1) conv_fwd_kernel(ConvArgs a) {
     constexpr int NP = Pairs<V>::N, U = kConvFwdU, GR = kConvFwdGroups;
     using Ring = ConvRing<T, V, U, GR>;
     constexpr bool kStaged = V == 4;

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(NormArgs a) {
 // needed): kDepth rows of three tensors.  Without vectors (V = 1) the next row waits in registers.
 template <int V, int NV, int NT>
 struct NormRing {
-    static constexpr int kDepth = V == 1 ? 0 : NV * NT <= 1024 ? 3 : NV * NT <= 2048 ? 2 : 1;
+    static constexpr int kDepth = V == 1 ? 0 : NV * NT <= 256 ? 4 : NV * NT <= 1024 ? 3 : NV * NT <= 2048 ? 2 : 1;
     static constexpr size_t kBytes = (size_t)kDepth * 3 * NV * NT * 16;
 };
 
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(int blocks, int D, const
     const int c = blockIdx.x * 32 + lane;
     double s = 0.0;
     if (c < D)
-#pragma unroll 4
+#pragma unroll 8
         for (int k = wy; k < blocks; k += 32) s += (double)part[((size_t)k * 2 + blockIdx.y) * D + c];
     red[wy][lane] = s;
     __syncthreads();

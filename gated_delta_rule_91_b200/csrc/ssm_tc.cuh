@@ -400,7 +400,10 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
 
 // ---- 3. outputs ------------------------------------------------------------------------------
 // LO: the state's own product takes both parts of w B, and S_T is written at the end (one segment).  With P = 64 two
-// CTAs of 8 warps share an SM; with P = 128 (the shared memory of one) a CTA has 16.
+// CTAs of 8 warps share an SM; with P = 128 (the shared memory of one) a CTA has 16.  A chunk takes about 8700 cycles at
+// P = N = 128 (84 us at B=4 T=4096 H=16): each of its two rounds of products waits for register conversions and two
+// barriers.  The next chunk's K formed behind this chunk's last products, with B, C and K in two stages, took 94 us: the
+// conversions, not the products, are what the chunk waits for.
 template <int P, int N, bool LO>
 struct SsmYTc {
     static constexpr int NT = P == 128 ? 512 : 256, kParts = NT / 128;  // warps of one TMEM quarter: column parts

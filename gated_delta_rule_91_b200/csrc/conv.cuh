@@ -2,10 +2,14 @@
 // depthwise over C channels, width K <= 8, optional bias and SiLU, the last
 // K-1 inputs carried between calls (a decode token is T = 1):
 //     z[t,c] = bias[c] + sum_{j<K} w[c,j] x[t-K+1+j, c],   y = z sigmoid(z) or z
-// HBM-bound: x is read and y written once.  A thread owns V = 4 neighbouring
-// channels (8 bytes of bf16: with 8 its windows leave one block a SM) and walks a run of
-// tokens with the last K-1 inputs in registers, so that only the K-1 inputs
-// before a run are read a second time, from L2.
+// HBM-bound by its bytes: x is read and y written once.  A thread owns V = 4
+// neighbouring channels (8 bytes of bf16: with 8 its windows leave one block a
+// SM) and walks a run of tokens with the last K-1 inputs in registers, so that
+// only the K-1 inputs before a run are read a second time, from L2.  B=4 T=4096
+// C=2304 K=4 bf16: forward 37 us (4.1 TB/s; 23 issue slots an element are its
+// bound now), backward 66 us (3.4 TB/s; 12 warps a SM, since its two windows,
+// the taps and their sums take 165 registers: held to 128 it spilled, 70 us,
+// held to 96 it took 151 us).
 #pragma once
 #include "common.cuh"
 
@@ -299,12 +303,13 @@ __global__ void __launch_bounds__(256, K <= 4 ? 3 : 1) conv_fwd_kernel(ConvArgs 
 }
 
 // Backward.  dz_t = dy_t silu'(z_t); dx_s = sum_j w_j dz_{s+K-1-j}; dw_j = sum_t dz_t x_{t-K+1+j}.
-// A block is 32 channel groups x 8 runs; each of the 8 walks its runs (a slot's runs are slots*8 apart) and the
-// eight tap sums are joined in shared memory in a fixed order before one partial row per slot is written.  A run's
+// A block is 32 channel groups x 4 runs; each of the 4 walks its runs (a slot's runs are slots*4 apart) and the
+// four tap sums are joined in shared memory in a fixed order before one partial row per slot is written.  A run's
 // first K-1 tokens emit no dx of their own run, and K-1 tokens past its end only finish it; the tokens between
 // take no checks (with them everywhere the kernel ran 85 instructions an element and 135 us at B=4 T=4096 C=2304).
+constexpr int kConvBwdWarps = 4;
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(256, K <= 4 ? 2 : 1) conv_bwd_kernel(ConvArgs a, int slots) {
+__global__ void __launch_bounds__(kConvBwdWarps * 32, K <= 4 ? 3 : 2) conv_bwd_kernel(ConvArgs a, int slots) {
     constexpr int NP = Pairs<V>::N, U = kConvBwdU, GR = kConvBwdGroups;
     using Ring = ConvRing<T, V, U, GR>;
     constexpr bool kStaged = V == 4;
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(256, K <= 4 ? 2 : 1) conv_bwd_kernel(ConvArgs 
         bias = conv_bias<V>(a.bias, c);
     }
     const long long nruns = (long long)a.runs * a.B;
-    for (long long q = (long long)slot * 8 + wy; q < nruns; q += (long long)slots * 8) {
+    for (long long q = (long long)slot * kConvBwdWarps + wy; q < nruns; q += (long long)slots * kConvBwdWarps) {
         const int r = (int)(q % a.runs), b = (int)(q / a.runs);
         const int t0 = r * a.run, t1 = min(a.T, t0 + a.run), tend = t1 + K - 1;
         T *pd = static_cast<T *>(a.dx) + ((size_t)b * a.T + t0) * a.C + c;  // dx of the run's next token
@@ -467,11 +472,11 @@ __global__ void __launch_bounds__(256, K <= 4 ? 2 : 1) conv_bwd_kernel(ConvArgs 
         red[wy][K][lane * V + i] = (i & 1) ? ab.p[i / 2].y : ab.p[i / 2].x;
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < (K + 1) * 32 * V; k += 256) {
+    for (int k = threadIdx.x; k < (K + 1) * 32 * V; k += kConvBwdWarps * 32) {
         const int j = k / (32 * V), i = k % (32 * V), ch = blockIdx.x * 32 * V + i;
         if (ch >= a.C) continue;
         float s = 0.f;
-        for (int y = 0; y < 8; ++y) s += red[y][j][i];
+        for (int y = 0; y < kConvBwdWarps; ++y) s += red[y][j][i];
         a.part[((size_t)slot * (K + 1) + j) * a.C + ch] = s;
     }
 }
@@ -497,12 +502,12 @@ __global__ void __launch_bounds__(256) conv_sum_kernel(int slots, int K, int C, 
 }
 
 // ---- host side ------------------------------------------------------------------------------
-// Slots of the backward: the blocks (32 V channels x 8 runs) that fit the SMs at once, two each; bounded by the runs.
+// Slots of the backward: the blocks (32 V channels x 4 runs) that fit the SMs at once, three each; bounded by the runs.
 inline int conv_bwd_slots(int B, int T, int C, int V, int run) {
     const long long runs = (long long)((T + run - 1) / run) * B;
     const long long cols = (C + 32 * V - 1) / (32 * V);
-    long long s = (148 * 2) / cols;
-    const long long most = (runs + 7) / 8;
+    long long s = (148 * 3) / cols;
+    const long long most = (runs + kConvBwdWarps - 1) / kConvBwdWarps;
     if (s > most) s = most;
     return (int)(s < 1 ? 1 : s);
 }
@@ -525,11 +530,11 @@ cudaError_t conv_bwd_launch(ConvArgs a, float *dw, float *dbias, cudaStream_t s)
     a.run = kConvBwdRun;
     a.runs = (a.T + a.run - 1) / a.run;
     const int slots = conv_bwd_slots(a.B, a.T, a.C, V, a.run);
-    const size_t rings = V == 4 ? (size_t)16 * ConvRing<T, V, kConvBwdU, kConvBwdGroups>::kBytes : 0, red = (size_t)8 * (K + 1) * 32 * V * 4;
+    const size_t rings = V == 4 ? (size_t)2 * kConvBwdWarps * ConvRing<T, V, kConvBwdU, kConvBwdGroups>::kBytes : 0, red = (size_t)kConvBwdWarps * (K + 1) * 32 * V * 4;
     const size_t smem = rings > red ? rings : red;
     cudaError_t e = cudaFuncSetAttribute(conv_bwd_kernel<T, V, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    conv_bwd_kernel<T, V, K><<<dim3((a.C + 32 * V - 1) / (32 * V), slots), 256, smem, s>>>(a, slots);
+    conv_bwd_kernel<T, V, K><<<dim3((a.C + 32 * V - 1) / (32 * V), slots), kConvBwdWarps * 32, smem, s>>>(a, slots);
     conv_sum_kernel<<<dim3((a.C + 31) / 32, K + 1), 256, 0, s>>>(slots, K, a.C, a.part, dw, dbias);
     g_launches.fetch_add(2, std::memory_order_relaxed);
     return cudaGetLastError();

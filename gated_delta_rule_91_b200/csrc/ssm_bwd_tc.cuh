@@ -639,8 +639,10 @@ cudaError_t ssm_tc_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     if (e == cudaSuccess && w.R > 1) {
         e = ssm_launch(ssm_tc_walk_kernel<P, N, false>, grid, SsmWalkTc<P, N>::kThreads, smem, s, mx, mb, my, mc, ms, mg, a, w.m, 2,
                        (const float *)gates, segS, segG, dec);
-        if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, w.R, a.H, P * N, segS, dec, a.S0, nullptr, s);
-        if (e == cudaSuccess) e = ssm_launch_scan(true, a.B, w.R, a.H, P * N, segG, dec, a.dS_T, nullptr, s);
+        if (e == cudaSuccess && w.R > kJoinMost) {
+            e = ssm_launch_scan(false, a.B, w.R, a.H, P * N, segS, dec, a.S0, nullptr, s);
+            if (e == cudaSuccess) e = ssm_launch_scan(true, a.B, w.R, a.H, P * N, segG, dec, a.dS_T, nullptr, s);
+        }
     }
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_walk_kernel<P, N, true>, grid, SsmWalkTc<P, N>::kThreads, smem, s, mx, mb, my, mc, ms, mg, a, w.m, 2,

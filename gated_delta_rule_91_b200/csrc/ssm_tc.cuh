@@ -21,7 +21,7 @@
 //   0. ssm_gate_kernel      the decays of every chunk and head as tables
 // A long sequence over few heads is cut into segments of whole chunks:
 //   1. ssm_tc_walk_kernel   a segment's own sum of w_j x_j B_j^T, decayed to its end
-//   2. ssm_scan_kernel      the states between the segments, elementwise, fp32
+//   2. ssm_scan_kernel      the states between many segments, elementwise, fp32
 //   3. ssm_tc_y_kernel      walks its segment from that state
 // One segment alone is 0 and 3, with the state written at its end.
 #pragma once
@@ -157,6 +157,37 @@ inline bool ssm_state_map(CUtensorMap *map, const void *base, size_t units, int 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Up to this many segments are joined by every reader itself (it reads the sums of the segments before its own);
+// ssm_scan_kernel joins more.  B=4 T=4096 H=16 P=N=128, 2 segments: @J1@ us, with the scan's launch 144 us.
+constexpr int kJoinMost = 8;
+
+// The state entering segment seg (leaving it, rev), columns cp .. cp + W - 1 of row n: from the scanned segments, or
+// joined here from the segments' own sums and decays.
+template <int W, int P, int N>
+__device__ __forceinline__ void ssm_enter_segment(float (&v)[W], const float *segs, const float *dec, const float *first,
+                                                  int R, int seg, int b, int h, int H, int cp, int n, bool rev) {
+    const bool on = n < N;
+    auto load = [&](const float *src, float (&x)[W]) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] = src && on ? src[(size_t)(cp + i) * N + n] : 0.f;
+    };
+    if (R > kJoinMost) {
+        load(segs + (((size_t)b * R + seg) * H + h) * P * N, v);
+        return;
+    }
+    load(first ? first + ((size_t)b * H + h) * P * N : nullptr, v);
+    const int before = rev ? R - 1 - seg : seg;
+#pragma unroll 1
+    for (int k = 0; k < before; ++k) {
+        const size_t unit = ((size_t)b * R + (rev ? R - 1 - k : k)) * H + h;
+        float x[W];
+        load(segs + unit * P * N, x);
+        const float d = dec[unit];
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = fmaf(d, v[i], x[i]);
+    }
+}
+
 // A CTA walks the chunks of one (b, h, segment), forwards (S <- e^{c_last} S + B^T (w X)) or, rev, backwards (G <-
 // e^{c_last} G + C^T (e^c dY)), the state in TMEM (lanes n, columns p, fp32), the weighted rows in two bf16 parts.
 // OUT: from the state that enters the segment, every chunk's entering state is written as two bf16 parts (out_S, out_G
@@ -284,13 +315,11 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     };
     float v[PW];
     {
-        const float *src = nullptr;
-        if (OUT) {
-            if (R > 1) src = (rev ? seg_G : seg_S) + (((size_t)b * R + seg) * a.H + h) * P * N;
-            else if (rev ? a.dS_T : a.S0) src = (rev ? a.dS_T : a.S0) + (size_t)bh * P * N;
-        }
+        if (OUT)
+            ssm_enter_segment<PW, P, N>(v, rev ? seg_G : seg_S, dec, rev ? a.dS_T : a.S0, R, seg, b, h, a.H, cp, row, rev);
+        else
 #pragma unroll
-        for (int i = 0; i < PW; ++i) v[i] = src && row < N ? src[(size_t)(cp + i) * N + row] : 0.f;
+            for (int i = 0; i < PW; ++i) v[i] = 0.f;
         tmem_stw<PW>(tl, v);
         tmem_wait_st();
     }
@@ -423,7 +452,7 @@ template <int P, int N, bool LO>
 __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) ssm_tc_y_kernel(
     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y, SsmArgs a, int m,
-    const float *__restrict__ gates, const float *__restrict__ states) {
+    const float *__restrict__ gates, const float *__restrict__ states, const float *__restrict__ dec) {
     using L = SsmYTc<P, N, LO>;
     using namespace sm100;
     extern __shared__ uint8_t smem_raw[];
@@ -493,10 +522,17 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
     }
     __syncwarp();
     {   // the entering state: lane n, columns p
-        const float *src = states ? states + (((size_t)b * R + seg) * a.H + h) * P * N : a.S0 ? a.S0 + (size_t)bh * P * N : nullptr;
         float v[32];
+        ssm_enter_segment<32, P, N>(v, states, dec, a.S0, R, seg, b, h, a.H, cp, row, false);
+        if (!LO && R <= kJoinMost && seg == R - 1 && a.S_T && row < N) {  // the last segment's end, in fp32
+            const size_t unit = ((size_t)b * R + seg) * a.H + h;
+            const float d = dec[unit];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = src && row < N ? src[(size_t)(cp + i) * N + row] : 0.f;
+            for (int i = 0; i < 32; ++i) {
+                const size_t at = (size_t)(cp + i) * N + row;
+                a.S_T[(size_t)bh * P * N + at] = fmaf(d, v[i], states[unit * P * N + at]);
+            }
+        }
         tmem_st32(tl + tS + cp, v);
         tmem_wait_st();
     }
@@ -789,15 +825,15 @@ cudaError_t ssm_tc_fwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (R == 1)
         return ssm_launch(ssm_tc_y_kernel<P, N, true>, grid, SsmYTc<P, N, true>::NT, (size_t)SsmYTc<P, N, true>::kAlloc, s, mx,
-                          mb, mc, my, a, m, (const float *)gates, (const float *)nullptr);
+                          mb, mc, my, a, m, (const float *)gates, (const float *)nullptr, (const float *)nullptr);
     float *st = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.st);
     float *dec = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.dec);
     e = ssm_launch(ssm_tc_walk_kernel<P, N, false>, grid, SsmWalkTc<P, N>::kThreads, (size_t)SsmWalkTc<P, N>::kAlloc, s, mx, mb,
                    mx, mb, mx, mx, a, m, 1, (const float *)gates, st, (float *)nullptr, dec);
-    if (e == cudaSuccess) e = ssm_launch_scan(false, a.B, R, a.H, P * N, st, dec, a.S0, a.S_T, s);
+    if (e == cudaSuccess && R > kJoinMost) e = ssm_launch_scan(false, a.B, R, a.H, P * N, st, dec, a.S0, a.S_T, s);
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_y_kernel<P, N, false>, grid, SsmYTc<P, N, false>::NT, (size_t)SsmYTc<P, N, false>::kAlloc, s, mx,
-                       mb, mc, my, a, m, (const float *)gates, (const float *)st);
+                       mb, mc, my, a, m, (const float *)gates, (const float *)st, (const float *)dec);
     return e;
 }
 

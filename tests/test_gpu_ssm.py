@@ -107,6 +107,31 @@ def test_many_chunks(dtype):
     check_bwd(d, bwd(d))
 
 
+@pytest.mark.parametrize("T,P", [(500, 128), (700, 64), (1100, 64), (2300, 128)])
+def test_segments_joined_by_readers_and_by_a_scan(T, P):
+    """Few and many segments: 4 to 18 chunks of one sequence."""
+    d = inputs(1, T, 2, 2, P, 64, "bf16", seed=T)
+    check_fwd(d, *fwd(d))
+    check_bwd(d, bwd(d))
+    d["S0"] = d["dS_T"] = None
+    check_fwd(d, *fwd(d))
+    check_bwd(d, bwd(d))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_state_without_its_gradient_and_strided_leaves(dtype):
+    """S0 given and S_T unused; x, B and C in an order that the library does not read in place."""
+    d = inputs(2, 100, 2, 2, 64, 64, dtype, seed=21)
+    d["dS_T"] = None
+    check_bwd(d, bwd(d))
+    odd = {k: d[k].transpose(1, 2).contiguous().transpose(1, 2) for k in ("x", "Bm", "Cm")}
+    assert not odd["x"].is_contiguous()
+    leaf = odd["x"].detach().requires_grad_()
+    y, _ = ag.selective_scan(leaf, d["delta"], d["A"], odd["Bm"], odd["Cm"], d["D"], d["bias"], d["S0"], softplus=True)
+    y.backward(d["dy"])
+    assert torch.equal(y.detach(), fwd(d)[0]) and torch.equal(leaf.grad, bwd(d)["dx"])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_without_bias_skip_state_and_softplus(dtype):
     d = inputs(1, 140, 2, 2, 64, 64, dtype, seed=3, s0=False)

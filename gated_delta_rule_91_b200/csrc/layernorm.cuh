@@ -339,10 +339,11 @@ constexpr int kNormBwdMaxBlocks = 148 * 8;
 
 // Calls F<V, TPR, NV, NT>: vectors of 16 bytes where D allows, else single elements.  The fewest threads per row
 // that hold it in at most 16 elements a thread, a warp where that is enough: a thread's exchanges with the others are
-// then spread over 16 elements, and the backward's five arrays of them still fit its registers.
+// then spread over 16 elements, and the backward's five arrays of them still fit its registers (single elements are half
+// a pair each, so 4 of them: 18304 x 1333 fp32 took 369 us with 8, in blocks of 512 threads that spilled).
 template <typename T, bool BWD, template <typename, int, int, int, int> class F, typename... A>
 cudaError_t norm_pick(int D, A... args) {
-    constexpr int V = sizeof(T) == 2 ? 8 : 4, M = 16, S = BWD ? 8 : 16;
+    constexpr int V = sizeof(T) == 2 ? 8 : 4, M = 16, S = BWD ? 4 : 16;
     if (D % V == 0) {
         if (D <= 32 * V) return F<T, V, 32, 1, 256>::go(args...);
         if (D <= 32 * M) return F<T, V, 32, M / V, 256>::go(args...);
@@ -353,7 +354,9 @@ cudaError_t norm_pick(int D, A... args) {
     }
     if (D <= 32 * S) return F<T, 1, 32, S, 256>::go(args...);
     if (D <= 128 * S) return F<T, 1, 128, S, 128>::go(args...);
+    if (D <= 256 * S) return F<T, 1, 256, S, 256>::go(args...);
     if (D <= 512 * S) return F<T, 1, 512, S, 512>::go(args...);
+    if (D <= 512 * 8) return F<T, 1, 512, 8, 512>::go(args...);
     if (D <= 512 * 16) return F<T, 1, 512, 16, 512>::go(args...);
     return F<T, 1, 512, kNormMaxD / 512, 512>::go(args...);
 }

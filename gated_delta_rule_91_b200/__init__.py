@@ -404,6 +404,12 @@ def _like(name, t, shape, dtype, device):
     return t.data_ptr()
 
 
+def _ints(*sizes):
+    """Sizes and strides are C ints: a larger one would wrap on its way into the library."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError("sizes and strides must be below 2^31, got %s" % (sizes,))
+
+
 def _rows(name, t, shape, lead, dtype, device):
     """`t` as rows of a wider buffer: the axes from `lead` on are a dense row, and the rows of the leading axes are
     one stride apart.  Returns (address, stride in elements; 0: dense)."""
@@ -427,6 +433,7 @@ def _rows(name, t, shape, lead, dtype, device):
             elif strides[i] != rows * ld:
                 raise ValueError("%s: the rows of all batches must be one stride apart" % name)
             rows *= shape[i]
+    _ints(ld)
     return t.data_ptr(), ld
 
 
@@ -530,6 +537,7 @@ def _conv_operands(x, w, bias, conv_state):
         raise ValueError("x must be [B,T,C] and w [C,K], got %s and %s" % (tuple(x.shape), tuple(w.shape)))
     B, T, C = x.shape
     K = w.shape[1]
+    _ints(B, T, C, K)
     px, ldx = _rows("x", x, x.shape, 2, x.dtype, dev)
     return (B, T, C, K, dt, dev, (px, ldx, _like("w", w, (C, K), torch.float32, dev),
                                   _like("bias", bias, (C,), torch.float32, dev),
@@ -571,6 +579,7 @@ def gdr_layernorm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, 
     """Layer norm of h = x + residual over the last axis (x [...,D]; weight, bias [D] fp32).  Returns (y, h); h is
     None without a residual."""
     dev, dt, D = _cuda(x, "x"), _dt(x), x.shape[-1]
+    _ints(D)
     y = x.new_empty(x.shape) if y is None else y
     if residual is not None and h is None:
         h = torch.empty(x.shape, dtype=x.dtype, device=dev)
@@ -587,6 +596,7 @@ def gdr_layernorm_bwd(h, weight, dy, *, dres=None, eps=1e-5, want_dbias=True, wo
     """Backward of gdr_layernorm_fwd from the stored stream h (x without a residual) and the gradient dres that
     reaches h along the residual stream.  Returns (dx, dweight, dbias or None)."""
     dev, dt, D = _cuda(h, "h"), _dt(h), h.shape[-1]
+    _ints(D)
     f = torch.float32
     dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
     dweight = torch.empty(D, dtype=f, device=dev)

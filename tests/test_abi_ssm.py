@@ -91,3 +91,31 @@ def test_workspace_sizes():
     assert L.gdr_ssm_bwd_workspace_bytes(1, 100, 1, 1, 64, 64, 0) > 0
     assert L.gdr_conv_bwd_workspace_bytes(1, 10, 8, 9) == 0 and L.gdr_conv_bwd_workspace_bytes(1, 10, 8, 4) > 0
     assert L.gdr_layernorm_bwd_workspace_bytes(0) == 0 and L.gdr_layernorm_bwd_workspace_bytes(16384) > 0
+
+
+def test_sizes_that_wrap_in_32_bits(monkeypatch):
+    """2^32 + 1 tokens of one channel are no single token: sizes and strides past a C int are refused in the binding."""
+    import torch
+    monkeypatch.setattr(gdr, "_cuda", lambda x, name: x.device)
+    meta = dict(dtype=torch.bfloat16, device="meta")
+    w = torch.empty(1, 4, device="meta")
+    for x in (torch.empty(1, (1 << 32) + 1, 1, **meta), torch.empty_strided((2, 1, 1), ((1 << 32) + 8, 8, 1), **meta)):
+        with pytest.raises(ValueError, match="below 2"):
+            gdr.gdr_conv_fwd(x, w)
+        with pytest.raises(ValueError, match="below 2"):
+            gdr.gdr_conv_bwd(x, w, x)
+    with pytest.raises(ValueError, match="below 2"):
+        gdr.gdr_conv_fwd(torch.empty(1, 4, 1, **meta), torch.empty(1, (1 << 32) + 4, device="meta"))
+    x, v = torch.empty(1, (1 << 32) + 1, **meta), torch.empty((1 << 32) + 1, device="meta")
+    with pytest.raises(ValueError, match="below 2"):
+        gdr.gdr_layernorm_fwd(x, v)
+    with pytest.raises(ValueError, match="below 2"):
+        gdr.gdr_layernorm_bwd(x, v, x)
+    rows = torch.empty_strided((2, 1, 64), ((1 << 32) + 64, 64, 1), **meta)
+    small = torch.empty(2, 1, 64, **meta)
+    f = dict(device="meta")
+    with pytest.raises(ValueError, match="below 2"):
+        gdr.gdr_ssm_step(rows, torch.empty(2, 1, **f), torch.empty(1, **f), small, small, torch.empty(2, 1, 64, 64, **f))
+    L = gdr.lib()
+    assert L.gdr_conv_fwd(1, (1 << 31) - 1, 1, 4, gdr.GDR_BF16, 1, P(FAKE), 0, P(FAKE), None, None, None, P(2 * FAKE), None) == UNS
+    assert L.gdr_conv_bwd_workspace_bytes(1, (1 << 31) - 1, 1, 4) == 0

@@ -4,6 +4,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "abi_common.cuh"
 #include "conv.cuh"
 #include "layernorm.cuh"
@@ -47,6 +49,14 @@ gdr_status check_ssm_grid(const char *fn, int B, int T, int H, int G, int P, int
     if (st == GDR_OK && (B > 65535 || H > 65535))
         return fail(GDR_ERR_UNSUPPORTED, "%s: B=%d H=%d (at most 65535 each)", fn, B, H);
     return st;
+}
+
+// An output at an input's own address (the kernels read inputs again after the first outputs are written).
+bool in_place(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
+    for (const void *o : outs)
+        for (const void *i : ins)
+            if (o != nullptr && o == i) return true;
+    return false;
 }
 
 // Token stride `ld` of `width` elements: 0 means dense; rows start on 16-byte boundaries.
@@ -134,6 +144,8 @@ gdr_status gdr_ssm_fwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, i
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(GDR_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
     GDR_OPTIONAL_PTR(workspace);
+    if (in_place({y, S_T}, {x, delta, A, Bm, Cm, D, delta_bias, S0}))
+        return fail(GDR_ERR_INVALID_ARGUMENT, "%s: an output is an input", fn);
     SsmArgs a{};
     a.B = B; a.T = T; a.H = H; a.G = G; a.P = P; a.N = N;
     a.x = x; a.Bm = Bm; a.Cm = Cm; a.ldx = ldx; a.ldb = ldb; a.ldc = ldc;
@@ -185,6 +197,8 @@ gdr_status gdr_ssm_bwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, i
     if (workspace == nullptr || workspace_bytes < need)
         return fail(GDR_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
     if (!aligned16(workspace)) return fail(GDR_ERR_INVALID_ARGUMENT, "%s: workspace is not 16-byte aligned", fn);
+    if (in_place({dx, ddelta, dA, dB, dC, dD, ddelta_bias, dS0}, {x, delta, A, Bm, Cm, D, delta_bias, S0, dy, dS_T}))
+        return fail(GDR_ERR_INVALID_ARGUMENT, "%s: an output is an input", fn);
     SsmArgs a{};
     a.B = B; a.T = T; a.H = H; a.G = G; a.P = P; a.N = N;
     a.x = x; a.Bm = Bm; a.Cm = Cm; a.ldx = ldx; a.ldb = ldb; a.ldc = ldc;
@@ -217,6 +231,8 @@ gdr_status gdr_ssm_step(int B, int H, int G, int P, int N, gdr_dtype dt, int sof
     GDR_OPTIONAL_PTR(delta_bias);
     GDR_REQUIRE_PTR(S);
     GDR_REQUIRE_PTR(y);
+    if (in_place({S, y}, {x, delta, A, Bm, Cm, D, delta_bias}))
+        return fail(GDR_ERR_INVALID_ARGUMENT, "%s: an output is an input", fn);
     SsmArgs a{};
     a.B = B; a.T = 1; a.H = H; a.G = G; a.P = P; a.N = N;
     a.x = x; a.Bm = Bm; a.Cm = Cm; a.ldx = ldx; a.ldb = ldb; a.ldc = ldc;
@@ -242,6 +258,8 @@ gdr_status gdr_conv_fwd(int B, int T, int C, int K, gdr_dtype dt, int silu, cons
     GDR_OPTIONAL_PTR(conv_state_in);
     GDR_OPTIONAL_PTR(conv_state_out);
     GDR_REQUIRE_PTR(y);
+    if (in_place({y}, {x, w, bias, conv_state_in}) || in_place({conv_state_out}, {x, w, bias}))
+        return fail(GDR_ERR_INVALID_ARGUMENT, "%s: an output is an input", fn);
     ConvArgs a{};
     a.B = B; a.T = T; a.C = C; a.ldx = ldx; a.silu = silu;
     a.x = x; a.w = w; a.bias = bias; a.y = y;
@@ -286,6 +304,8 @@ gdr_status gdr_conv_bwd(int B, int T, int C, int K, gdr_dtype dt, int silu, cons
     if (workspace == nullptr || workspace_bytes < need)
         return fail(GDR_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
     if (!aligned16(workspace)) return fail(GDR_ERR_INVALID_ARGUMENT, "%s: workspace is not 16-byte aligned", fn);
+    if (in_place({dx, dw, dbias, dconv_state_in}, {x, w, bias, conv_state_in, dy, dconv_state_out}))
+        return fail(GDR_ERR_INVALID_ARGUMENT, "%s: an output is an input", fn);
     ConvArgs a{};
     a.B = B; a.T = T; a.C = C; a.ldx = ldx; a.silu = silu;
     a.x = x; a.w = w; a.bias = bias; a.dy = dy; a.dx = dx;

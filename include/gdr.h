@@ -425,6 +425,8 @@ GDR_API gdr_status gdr_seg_fixup(int B, int T, int H, int dk, int dv, gdr_dtype 
  *   Supported: P, N in {64, 128}; H a multiple of G; B*T*H*max(P,N) < 2^31;
  *   B, H <= 65535.  workspace: gdr_ssm_fwd_workspace_bytes(...)
  *   bytes; NULL or short -> GDR_ERR_WORKSPACE.  Repeated calls give the same bits.
+ *   An output at the address of an input (S_T = S0, y = x) is refused, here and
+ *   in the scan's and the convolution's other calls.
  */
 GDR_API gdr_status gdr_ssm_fwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, int softplus,
                        const void *x, int ldx, const float *delta, const float *A,

@@ -119,3 +119,22 @@ def test_sizes_that_wrap_in_32_bits(monkeypatch):
     L = gdr.lib()
     assert L.gdr_conv_fwd(1, (1 << 31) - 1, 1, 4, gdr.GDR_BF16, 1, P(FAKE), 0, P(FAKE), None, None, None, P(2 * FAKE), None) == UNS
     assert L.gdr_conv_bwd_workspace_bytes(1, (1 << 31) - 1, 1, 4) == 0
+
+
+def test_outputs_in_place_are_refused():
+    L, a = gdr.lib(), [P(FAKE + 0x1000 * i) for i in range(24)]
+    s = (1, 4, 4, 2, 128, 64, gdr.GDR_BF16, 1)
+    ins = lambda v: (v[0], 0, v[1], v[2], v[3], 0, v[4], 0, v[5], v[6])  # noqa: E731
+    assert L.gdr_ssm_fwd(*s, *ins(a), a[7], a[8], a[7], a[9], 1 << 30, None) == BAD       # S_T = S0
+    assert L.gdr_ssm_fwd(*s, *ins(a), a[7], a[0], a[9], a[10], 1 << 30, None) == BAD      # y = x
+    assert L.gdr_ssm_step(s[0], *s[2:], *ins(a), a[7], a[0], None) == BAD                 # y = x
+    out = a[9:17]
+    for i, src in ((0, a[0]), (0, a[8]), (1, a[1]), (3, a[3]), (7, a[17])):               # dx = x, dx = dy, ..., dS0 = dS_T
+        assert L.gdr_ssm_bwd(*s, *ins(a), a[7], a[8], a[17], *(src if i == j else o for j, o in enumerate(out)), a[18], 1 << 30,
+                             None) == BAD
+        assert L.gdr_last_error_string().decode() == "gdr_ssm_bwd: an output is an input"
+    c = (1, 4, 40, 4, gdr.GDR_BF16, 1, a[0], 0, a[1], a[2], a[3])
+    assert L.gdr_conv_fwd(*c, a[4], a[0], None) == BAD and L.gdr_conv_fwd(*c, a[0], a[4], None) == BAD
+    assert L.gdr_conv_fwd(*c, a[4], a[3], None) == BAD                                    # y = the carried window
+    assert L.gdr_conv_bwd(*c, a[4], None, a[4], a[5], None, None, a[6], 1 << 30, None) == BAD
+    assert L.gdr_conv_bwd(*c, a[4], a[7], a[8], a[5], None, a[3], a[6], 1 << 30, None) == BAD

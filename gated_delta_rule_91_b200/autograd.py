@@ -11,9 +11,16 @@ zero gradients.  `block_prologue(...)` (ShortConv, SiLU, q/k L2) and
 block's steps around the recurrence, differentiated through
 gdr_block_prologue_bwd and gdr_block_epilogue_bwd.  `selective_scan(x, delta, A,
 Bm, Cm, ...)`, `short_conv(x, w, ...)` and `layer_norm(x, weight, ...)` wrap
-gdr_ssm_fwd, gdr_conv_fwd and gdr_layernorm_fwd with their backwards.
+gdr_ssm_fwd, gdr_conv_fwd and gdr_layernorm_fwd with their backwards, which
+have no gradients of their own (a second derivative is an error).
+
+A step may be captured in a CUDA graph.  torch ties the node that accumulates a
+leaf's gradient to the stream on which the first live graph of that leaf was
+built, so nothing of an eager step on the same leaves (its outputs, its loss)
+may be alive when a backward is captured.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (gdr2_bwd, gdr2_fwd, gdr_block_epilogue, gdr_block_epilogue_bwd, gdr_block_prologue,
                gdr_block_prologue_bwd, gdr_bwd, gdr_conv_bwd, gdr_conv_fwd, gdr_fwd, gdr_layernorm_bwd,
@@ -149,6 +156,7 @@ class SelectiveScan(torch.autograd.Function):
         return gdr_ssm_fwd(x, delta, A, Bm, Cm, D, delta_bias, S0, softplus=softplus)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dS_T):
         x, delta, A, Bm, Cm, D, delta_bias, S0 = ctx.saved_tensors
         g = gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, _c(dy), _c(dS_T), softplus=ctx.softplus,
@@ -172,6 +180,7 @@ class ShortConv(torch.autograd.Function):
         return gdr_conv_fwd(x, w, bias, conv_state=conv_state, silu=silu)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, bias, conv_state = ctx.saved_tensors
         g = gdr_conv_bwd(x, w, _c(dy), bias, conv_state=conv_state, silu=ctx.silu)
@@ -195,6 +204,7 @@ class LayerNorm(torch.autograd.Function):
         return y, h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         h, weight = ctx.saved_tensors
         dx, dweight, dbias = gdr_layernorm_bwd(h, weight, _c(dy), dres=_c(dh) if ctx.has_residual else None, eps=ctx.eps,

@@ -166,3 +166,106 @@ def test_two_captured_graphs_with_workspaces_of_their_own():
         torch.cuda.synchronize()
         for (y, S), (y2, S2) in zip(want, got):
             assert torch.equal(y, y2) and torch.equal(S, S2)
+
+
+def test_captured_training_step_replays_like_eager():
+    """Norm, convolution, scan and their gradients as one captured step over static buffers."""
+    g = torch.Generator().manual_seed(21)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    B, T, H, P, G, N, K = 2, 200, 2, 64, 1, 64, 4
+    C = H * P + 2 * G * N
+    leaves = [(0.5 * r(B, T, C)).bfloat16(), 1 + 0.1 * r(C), 0.1 * r(C), 0.5 * r(C, K), 0.1 * r(C), r(B, T, H),
+              -1 - torch.rand(H, generator=g), r(H)]
+    leaves = [v.cuda().requires_grad_() for v in leaves]
+    res, dy = r(B, T, C).bfloat16().cuda(), r(B, T, H, P).bfloat16().cuda()
+
+    def step():
+        x, nw, nb, w, b, delta, A, D = leaves
+        h, stream = ag.layer_norm(x, nw, nb, res)
+        c = ag.short_conv(h, w, b)
+        xs, bm, cm = c.split([H * P, G * N, G * N], -1)
+        y, _ = ag.selective_scan(xs.unflatten(-1, (H, P)), delta, A, bm.unflatten(-1, (G, N)), cm.unflatten(-1, (G, N)), D,
+                                 softplus=True)
+        torch.autograd.backward((y, stream), (dy, res))
+        return y.detach()
+
+    want = step().clone()
+    grads = [v.grad.clone() for v in leaves]
+    for v in leaves:
+        v.grad = None
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    for v in leaves:
+        v.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        got.zero_()
+        for v in leaves:
+            v.grad.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        for i, (v, e) in enumerate(zip(leaves, grads)):
+            assert torch.equal(v.grad, e), i
+
+
+def test_a_second_derivative_is_an_error():
+    x = torch.randn(2, 8, 16, device="cuda", requires_grad=True)
+    w = torch.randn(16, 4, device="cuda", requires_grad=True)
+    dx, = torch.autograd.grad(ag.short_conv(x, w).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()
+    n, = torch.autograd.grad(ag.layer_norm(x, torch.ones(16, device="cuda")).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        n.sum().backward()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_offsets_past_32_bits(dtype):
+    """Rows 2^16 elements apart: the last tokens start more than 2^31 elements behind the first.  The same as dense rows."""
+    g = torch.Generator().manual_seed(4)
+    B, T, H, P, G, N, ld, K = 1, 33000, 1, 64, 1, 64, 1 << 16, 4
+    C = H * P + 2 * G * N
+    wide = torch.empty(B, T, ld, dtype=dtype, device="cuda")
+    src = torch.randn(B, T, C, generator=g).to(dtype).cuda()
+    wide[..., :C] = src
+    w = torch.randn(C, K, generator=g).cuda()
+    assert torch.equal(gdr.gdr_conv_fwd(wide[..., :C], w), gdr.gdr_conv_fwd(src, w))
+    a, b = gdr.gdr_conv_bwd(wide[..., :C], w, src), gdr.gdr_conv_bwd(src, w, src)
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dw"], b["dw"])
+    delta, A = torch.randn(B, T, H, generator=g).cuda(), torch.tensor([-1.5], device="cuda")
+
+    def cut(v):
+        x, bm, cm = v.split([H * P, G * N, G * N], -1)
+        return x.unflatten(-1, (H, P)), delta, A, bm.unflatten(-1, (G, N)), cm.unflatten(-1, (G, N))
+
+    dense = tuple(v.contiguous() for v in cut(src))
+    for p, q in zip(gdr.gdr_ssm_fwd(*cut(wide[..., :C]), softplus=True), gdr.gdr_ssm_fwd(*dense, softplus=True)):
+        assert torch.equal(p, q)
+    dy = dense[0].flip(1).contiguous()
+    a = gdr.gdr_ssm_bwd(*cut(wide[..., :C]), None, None, None, dy, softplus=True)
+    b = gdr.gdr_ssm_bwd(*dense, None, None, None, dy, softplus=True)
+    assert all(a[k] is None and b[k] is None or torch.equal(a[k], b[k]) for k in a)
+
+
+def test_states_past_32_bits():
+    """2^31 + 2^20 state elements in one step: the last batch advances as it does alone."""
+    g = torch.Generator().manual_seed(6)
+    H, P, N = 64, 128, 128
+    B = (1 << 31) // (H * P * N) + 1
+    r = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    x, bm, cm = r(B, H, P).bfloat16(), r(B, 1, N).bfloat16(), r(B, 1, N).bfloat16()
+    delta, A = r(B, H), -1 - torch.rand(H, generator=g).cuda()
+    S = torch.empty(B, H, P, N, device="cuda")
+    S[0], S[-1] = 1.0, 0.5
+    S[1:-1] = 0
+    y = gdr.gdr_ssm_step(x, delta, A, bm, cm, S, softplus=True)
+    for i, v in ((0, 1.0), (B - 1, 0.5)):
+        one = torch.full((1, H, P, N), v, device="cuda")
+        yi = gdr.gdr_ssm_step(x[i:i + 1], delta[i:i + 1], A, bm[i:i + 1], cm[i:i + 1], one, softplus=True)
+        assert torch.equal(yi, y[i:i + 1]) and torch.equal(one[0], S[i])

@@ -6,10 +6,11 @@
 // neighbouring channels (8 bytes of bf16: with 8 its windows leave one block a
 // SM) and walks a run of tokens with the last K-1 inputs in registers, so that
 // only the K-1 inputs before a run are read a second time, from L2.  B=4 T=4096
-// C=2304 K=4 bf16: forward 37 us (4.1 TB/s; 23 issue slots an element are its
-// bound now), backward 66 us (3.4 TB/s; 12 warps a SM, since its two windows,
-// the taps and their sums take 165 registers: held to 128 it spilled, 70 us,
-// held to 96 it took 151 us).
+// C=2304 K=4 bf16: forward 35 us (4.3 TB/s; 14 warp instructions an element, two
+// of them exponential and reciprocal: half of all issue slots and 55 % of that
+// unit's at 24 warps a SM), backward 57 us (4.0 TB/s; 12 warps a SM, since its
+// two windows, the taps and their sums take 165 registers: held to 128 it spilled
+// and lost 4 us, held to 96 it took 151 us).
 #pragma once
 #include "common.cuh"
 
@@ -503,19 +504,39 @@ __global__ void __launch_bounds__(256) conv_sum_kernel(int slots, int K, int C, 
 }
 
 // ---- host side ------------------------------------------------------------------------------
-// Slots of the backward: the blocks (32 V channels x 4 runs) that fit the SMs at once, three each; bounded by the runs.
-inline int conv_bwd_slots(int B, int T, int C, int V, int run) {
-    const long long runs = (long long)((T + run - 1) / run) * B;
+// Tokens per run of the forward: the shortest of 8, 16, .. 88 whose blocks are on the SMs all at once (blocks: how many
+// of the launch fit); a larger problem takes 64 of bf16, 32 of fp32.  A longer run reads fewer taps and windows, a
+// shorter one keeps more SMs at work.  C=2304 K=4: B=4 T=4096 bf16 36 us (88; 32: 39, 16: 43) and fp32 59 (32; 88: 66),
+// T=65536 bf16 111 us (64; 32: 119), T=512 10 us (16; 64: 16).
+inline int conv_fwd_run(int B, int T, int C, int V, int blocks, int otherwise) {
     const long long cols = (C + 32 * V - 1) / (32 * V);
-    long long s = (148 * 3) / cols;
-    const long long most = (runs + kConvBwdWarps - 1) / kConvBwdWarps;
-    if (s > most) s = most;
-    return (int)(s < 1 ? 1 : s);
+    for (int run = 8; run <= 88; run += 8)
+        if ((cols * ((T + run - 1) / run) * B + 7) / 8 <= blocks) return run;
+    return otherwise;
+}
+// The backward is one launch that fits (slots x columns, three blocks an SM up to K = 4); a warp's runs are as long as
+// their number stays the same for every warp and no run passes 192 tokens.  C=2304 K=4 bf16: B=4 T=4096 61 us (172;
+// 64, 2.7 runs a warp: 70), T=65536 199 us (172; 64: 219), T=512 18 us (16; 64: 23).
+struct ConvPlan {
+    int run, slots;
+};
+inline ConvPlan conv_bwd_plan(int B, int T, int C, int K, int V) {
+    const long long cols = (C + 32 * V - 1) / (32 * V), fit = 148 * (K <= 4 ? 3 : 2) / cols, room = fit < 1 ? 1 : fit;
+    const long long warps = room * kConvBwdWarps, need = (T + 191) / 192;
+    const long long trips = (B * need + warps - 1) / warps;
+    const long long runs = warps * trips / B;  // per sequence, at least `need`
+    const long long run = ((T + runs - 1) / runs + 3) / 4 * 4;
+    ConvPlan p;
+    p.run = run < 16 ? 16 : (int)run;
+    const long long most = ((long long)((T + p.run - 1) / p.run) * B + kConvBwdWarps - 1) / kConvBwdWarps;
+    p.slots = (int)(most < room ? most : room);
+    return p;
 }
 
 template <typename T, int V, int K>
 cudaError_t conv_fwd_launch(ConvArgs a, cudaStream_t s) {
-    a.run = 32;
+    // three blocks an SM of bf16 up to K = 4 (their bound on registers), two otherwise (the ring of fp32)
+    a.run = conv_fwd_run(a.B, a.T, a.C, V, 148 * (K <= 4 && sizeof(T) == 2 ? 3 : 2), sizeof(T) == 2 ? 64 : 32);
     a.runs = (a.T + a.run - 1) / a.run;
     const long long warps = (long long)((a.C + 32 * V - 1) / (32 * V)) * a.runs * a.B;
     const size_t smem = V == 4 ? (size_t)8 * ConvRing<T, V, kConvFwdU, kConvFwdGroups>::kBytes : 0;
@@ -525,12 +546,12 @@ cudaError_t conv_fwd_launch(ConvArgs a, cudaStream_t s) {
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cudaGetLastError();
 }
-constexpr int kConvBwdRun = 64;
 template <typename T, int V, int K>
 cudaError_t conv_bwd_launch(ConvArgs a, float *dw, float *dbias, cudaStream_t s) {
-    a.run = kConvBwdRun;
+    const ConvPlan plan = conv_bwd_plan(a.B, a.T, a.C, K, V);
+    const int slots = plan.slots;
+    a.run = plan.run;
     a.runs = (a.T + a.run - 1) / a.run;
-    const int slots = conv_bwd_slots(a.B, a.T, a.C, V, a.run);
     const size_t rings = V == 4 ? (size_t)2 * kConvBwdWarps * ConvRing<T, V, kConvBwdU, kConvBwdGroups>::kBytes : 0, red = (size_t)kConvBwdWarps * (K + 1) * 32 * V * 4;
     const size_t smem = rings > red ? rings : red;
     cudaError_t e = cudaFuncSetAttribute(conv_bwd_kernel<T, V, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

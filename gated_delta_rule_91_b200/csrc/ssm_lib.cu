@@ -278,8 +278,8 @@ gdr_status gdr_conv_fwd(int B, int T, int C, int K, gdr_dtype dt, int silu, cons
 size_t gdr_conv_bwd_workspace_bytes(int B, int T, int C, int K) {
     int ld = 0;
     if (check_conv("gdr_conv_bwd_workspace_bytes", B, T, C, K, GDR_F32, &ld) != GDR_OK) return 0;
-    // one bound for the vector and the scalar form: the scalar form has the fewer slots of a row each
-    const int slots = conv_bwd_slots(B, T, C, 4, kConvBwdRun), scalar = conv_bwd_slots(B, T, C, 1, kConvBwdRun);
+    // one bound for the vector and the scalar form
+    const int slots = conv_bwd_plan(B, T, C, K, 4).slots, scalar = conv_bwd_plan(B, T, C, K, 1).slots;
     return (size_t)(slots > scalar ? slots : scalar) * (K + 1) * C * sizeof(float);
 }
 

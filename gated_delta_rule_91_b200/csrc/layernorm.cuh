@@ -67,6 +67,36 @@ __device__ __forceinline__ void norm_reduce(float (&s)[NS], float *buf) {
     }
 }
 
+// The backward's row over two to four warps takes one barrier: each warp centres its values on its own mean, and the sums
+// are then moved to the row's (sum (h - m)^2 = sum (h - m_w)^2 + n_w (m_w - m)^2).  At 16384 x 2048 bf16 77 us, 84 with a
+// barrier for the mean and one for the sums; over 8 and 16 warps every thread's joining of them costs more than the
+// barrier (16384 x 4096: 152 us against 135), and so does the forward's.
+__device__ __forceinline__ float norm_warp_sum(float x) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+// Three sums over a warp, halving the values and the lanes that hold them together.  Lane l has the sum l / 8 (lanes from
+// 24 on: 0).
+__device__ __forceinline__ float norm_warp_sums(const float (&s)[4]) {
+    const int lane = threadIdx.x & 31;
+    const bool up = lane & 16, odd = lane & 8;
+    const float a = (up ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, up ? s[0] : s[2], 16);
+    const float b = (up ? 0.f : s[1]) + __shfl_xor_sync(0xffffffffu, up ? s[1] : 0.f, 16);
+    float v = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+#pragma unroll
+    for (int off = 4; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+// Columns of the row that its warp w holds.
+template <int V, int TPR, int NV>
+__device__ __forceinline__ float norm_warp_count(int w, int D) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) n += min(max(D - (i * TPR + w * 32) * V, 0), 32 * V);
+    return (float)n;
+}
+
 template <int V>
 __device__ __forceinline__ void norm_weights(const float *p, int c, float *v) {
     if (V == 8) {
@@ -162,6 +192,10 @@ struct NormRing {
 template <typename T, int V, int TPR, int NV, int NT>
 __global__ void __launch_bounds__(NT, V > 1 && V * NV <= 16 ? 512 / NT : 1) norm_bwd_kernel(NormArgs a) {
     constexpr int NP = Pairs<V>::N;
+    constexpr int W = TPR / 32;
+    constexpr bool kOne = W > 1 && W <= 4;  // one barrier a row
+    __shared__ float4 sums[kOne ? 2 * (NT / 32) : 1];  // rows take the two sides in turn
+    __shared__ float counts[W];
     __shared__ float buf[(NT / 32) * (1 + 4)];
     extern __shared__ __align__(16) float join[];  // the ring; at the end [NT/TPR][2][D] when NT > TPR
     uint4 *ring = reinterpret_cast<uint4 *>(join) + threadIdx.x;
@@ -183,6 +217,12 @@ __global__ void __launch_bounds__(NT, V > 1 && V * NV <= 16 ? 512 / NT : 1) norm
         }
     }
     const float inv = 1.f / (float)a.D;
+    float inv_own = inv;
+    if (kOne) {
+        const float n = norm_warp_count<V, TPR, NV>(tr >> 5, a.D);
+        inv_own = n > 0.f ? 1.f / n : 0.f;
+        if (threadIdx.x < W) counts[threadIdx.x] = norm_warp_count<V, TPR, NV>(threadIdx.x, a.D);  // read after a row's barrier
+    }
     const long long per = (long long)gridDim.x * (NT / TPR);
     const long long trips = (a.R + per - 1) / per;  // the same for every thread: the row sums use block barriers
     RowRaw<T, V> rh[NV], rg[NV], rd[NV];
@@ -251,8 +291,11 @@ __global__ void __launch_bounds__(NT, V > 1 && V * NV <= 16 ? 512 / NT : 1) norm
             fetch(row + per, a.dy, rg);
         }
         float m[1] = {s1.x + s1.y};
-        norm_reduce<TPR, NT, 1>(m, buf);
-        const float2 mean = make_float2(-m[0] * inv, V > 1 ? -m[0] * inv : 0.f);
+        if (kOne)
+            m[0] = norm_warp_sum(m[0]);
+        else
+            norm_reduce<TPR, NT, 1>(m, buf);
+        const float2 mean = make_float2(-m[0] * inv_own, V > 1 ? -m[0] * inv_own : 0.f);
         float2 ss = zero, sg = zero, sh = zero;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -267,12 +310,36 @@ __global__ void __launch_bounds__(NT, V > 1 && V * NV <= 16 ? 512 / NT : 1) norm
             }
         }
         float s[4] = {ss.x + ss.y, sg.x + sg.y, sh.x + sh.y, 0.f};
-        norm_reduce<TPR, NT, 4>(s, buf + NT / 32);
+        float shift = 0.f;  // the mean that h is centred on, less the row's
+        if (kOne) {
+            const float sum = norm_warp_sums(s);
+            const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp / W * W;
+            float4 *side = sums + (k & 1) * (NT / 32);
+            // lanes 0, 8, 16 write the sums, lane 24 the warp's mean
+            if (lane % 8 == 0) reinterpret_cast<float *>(&side[warp])[(lane / 8 + 1) & 3] = lane == 24 ? m[0] * inv_own : sum;
+            __syncthreads();
+            float row_mean = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) row_mean = fmaf(side[w0 + i].x, counts[i], row_mean);
+            row_mean *= inv;
+            s[0] = s[1] = s[2] = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float4 o = side[w0 + i];
+                const float d = o.x - row_mean;
+                s[0] += fmaf(d * d, counts[i], o.y);
+                s[1] += o.z;
+                s[2] += fmaf(d, o.z, o.w);
+            }
+            shift = m[0] * inv_own - row_mean;
+        } else {
+            norm_reduce<TPR, NT, 4>(s, buf + NT / 32);
+        }
         if (live) {
             const float rstd = 1.f / sqrtf(s[0] * inv + a.eps);
             // dx = rstd g w - rstd mean(g w) - (h - mean) rstd^3 mean(g w (h - mean))
-            const float b1 = -rstd * s[1] * inv, b2 = -rstd * rstd * (rstd * s[2] * inv);
-            const float2 r2 = make_float2(rstd, rstd), c1 = make_float2(b1, b1), c2 = make_float2(b2, b2);
+            const float b2 = -rstd * rstd * (rstd * s[2] * inv), b1 = fmaf(b2, shift, -rstd * s[1] * inv), sr = shift * rstd;
+            const float2 r2 = make_float2(rstd, rstd), c1 = make_float2(b1, b1), c2 = make_float2(b2, b2), s2 = make_float2(sr, sr);
             T *p = static_cast<T *>(a.dx) + (size_t)row * a.D + tr * V;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -283,7 +350,7 @@ __global__ void __launch_bounds__(NT, V > 1 && V * NV <= 16 ? 512 / NT : 1) norm
                 for (int e = 0; e < NP; ++e) {
                     float2 d = ffma2(fmul2(g[i].p[e], w[i].p[e]), r2, ffma2(h[i].p[e], c2, c1));
                     dx.p[e] = a.dres ? ffma2(d, one, dx.p[e]) : d;
-                    aw[i].p[e] = ffma2(g[i].p[e], fmul2(h[i].p[e], r2), aw[i].p[e]);
+                    aw[i].p[e] = ffma2(g[i].p[e], kOne ? ffma2(h[i].p[e], r2, s2) : fmul2(h[i].p[e], r2), aw[i].p[e]);
                     ab[i].p[e] = ffma2(g[i].p[e], one, ab[i].p[e]);
                 }
                 pairs_store<T, V>(p + i * TPR * V, dx);

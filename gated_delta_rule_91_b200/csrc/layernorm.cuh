@@ -58,11 +58,23 @@ __device__ __forceinline__ void norm_reduce(float (&s)[NS], float *buf) {
         if ((lane & ((32 >> LG) - 1)) == 0) buf[warp * NS + (lane >> (5 - LG))] = s[0];
         __syncthreads();
         const int w0 = warp / W * W;
+        if (W <= 4) {
 #pragma unroll
-        for (int k = 0; k < NS; ++k) {
-            s[k] = 0.f;
+            for (int k = 0; k < NS; ++k) {
+                s[k] = 0.f;
 #pragma unroll
-            for (int i = 0; i < W; ++i) s[k] += buf[(w0 + i) * NS + k];
+                for (int i = 0; i < W; ++i) s[k] += buf[(w0 + i) * NS + k];
+            }
+        } else {  // W NS reads and sums would cost more than the row's own arithmetic: 32 / NS lanes share a value's
+            constexpr int L = 32 / NS < W ? 32 / NS : W;
+            const int k = NS == 1 ? 0 : lane / L;
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; i += L) v += buf[(w0 + i + lane % L) * NS + k];
+#pragma unroll
+            for (int off = L / 2; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+#pragma unroll
+            for (int j = 0; j < NS; ++j) s[j] = NS == 1 ? v : __shfl_sync(0xffffffffu, v, j * L);
         }
     }
 }

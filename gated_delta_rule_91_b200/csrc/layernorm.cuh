@@ -198,9 +198,11 @@ struct NormRing {
     static constexpr size_t kBytes = (size_t)kDepth * 3 * NV * NT * 16;
 };
 
-// One block walks rows blockIdx.x * (NT/TPR) + rl, + gridDim.x * (NT/TPR), ...  Every thread keeps its columns' dw and db, and the block's row slots are joined in order at the end.
+// One block walks rows blockIdx.x * (NT/TPR) + rl, + gridDim.x * (NT/TPR), ...  Every thread keeps its columns' dw and
+// db, and the block's row slots are joined in order at the end.
 // The arithmetic is on packed pairs: as scalars it took 59 instructions an element.  16384 x 2048 bf16 with dres:
-// 125 us as scalars, 70 us with the next row in registers.
+// 125 us as scalars.  A row stays in registers between its passes: read again from the ring, with the weights in shared
+// memory and 20 or 24 warps an SM rather than 16, it took 83 us with cold caches (77 as it is).
 template <typename T, int V, int TPR, int NV, int NT>
 __global__ void __launch_bounds__(NT, V > 1 && V * NV <= 16 ? 512 / NT : 1) norm_bwd_kernel(NormArgs a) {
     constexpr int NP = Pairs<V>::N;

@@ -7,9 +7,9 @@
 // HBM-bound: every row is read once into registers (raw, as stored) and both
 // statistics are taken from there, the variance from centred values.  TPR
 // threads share a row and hold NV vectors of V elements each.  16384 x 2048
-// bf16 with the residual stream: forward 45 us (5.9 TB/s), backward 73 us (3.7
-// TB/s: 61 us of rows at 16 warps a SM, bound by their exchanges, and the sum of
-// the blocks' partial rows).
+// bf16 with the residual stream: forward 47 us (5.7 TB/s), backward 68 us (3.9
+// TB/s: rows at 16 warps a SM, bound by their exchanges and half of all issue
+// slots, and 7 us for the sum of the blocks' partial rows).
 #pragma once
 #include "common.cuh"
 #include "conv.cuh"

@@ -123,3 +123,9 @@ def test_workspace_and_refusals():
             gdr.gdr_conv_fwd(**{**dict(x=d["x"], w=d["w"], bias=d["bias"]), **bad})
     with pytest.raises(gdr.GdrError):
         gdr.gdr_conv_fwd(d["x"], torch.zeros(40, 9, device="cuda"))
+
+
+@pytest.mark.parametrize("B,T,C,K,dtype", [(5000, 3, 64, 4, "bf16"), (1, 100000, 8, 4, "bf16"), (3, 17, 50001, 2, "f32"),
+                                           (97, 193, 64, 4, "bf16"), (96, 192, 64, 8, "bf16"), (2, 30000, 20, 7, "f32")])
+def test_runs_of_many_sequences_long_ones_and_many_channels(B, T, C, K, dtype):
+    check(inputs(B, T, C, K, dtype, bias=True, state=True, extra=8, seed=1), True)

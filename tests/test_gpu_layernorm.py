@@ -102,3 +102,10 @@ def test_refusals():
         gdr.gdr_layernorm_fwd(torch.zeros(1, 16385, device="cuda"), torch.zeros(16385, device="cuda"))
     with pytest.raises(gdr.GdrError):
         gdr.gdr_layernorm_bwd(d["x"], d["w"], d["dy"], workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("R,D,dtype", [(3, 513, "bf16"), (700, 520, "bf16"), (900, 1032, "bf16"), (300, 516, "f32"), (300, 2052, "f32"),
+                                       (100, 4104, "bf16"), (40, 6000, "bf16"), (61, 16383, "bf16")])
+def test_rows_that_leave_warps_short(R, D, dtype):
+    """The last warps of a row hold fewer columns or none; the mean (5) is far from zero."""
+    check(inputs(R, D, dtype, seed=2, mean=5), True, True, 1e-5)

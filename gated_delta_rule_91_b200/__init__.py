@@ -71,6 +71,7 @@ SIGNATURES = {
     "gdr_ssm_fwd_workspace_bytes": (_SZ, [_I] * 7),
     "gdr_ssm_bwd": (_I, [_I] * 8 + [_P, _I, _P, _P, _P, _I, _P, _I] + [_P] * 13 + [_P, _SZ, _P]),
     "gdr_ssm_bwd_workspace_bytes": (_SZ, [_I] * 7),
+    "gdr_debug_ssm_plan": (_I, [_I] * 6 + [_P]),
     "gdr_ssm_step": (_I, [_I] * 7 + [_P, _I, _P, _P, _P, _I, _P, _I] + [_P] * 4 + [_P]),
     "gdr_conv_fwd": (_I, [_I] * 6 + [_P, _I] + [_P] * 5 + [_P]),
     "gdr_conv_bwd": (_I, [_I] * 6 + [_P, _I] + [_P] * 9 + [_P, _SZ, _P]),

@@ -213,6 +213,22 @@ gdr_status gdr_ssm_bwd(int B, int T, int H, int G, int P, int N, gdr_dtype dt, i
     return GDR_OK;
 }
 
+gdr_status gdr_debug_ssm_plan(int B, int T, int H, int G, int P, int N, int *plan) {
+    const char *fn = "gdr_debug_ssm_plan";
+    gdr_status st = check_ssm_grid(fn, B, T, H, G, P, N, GDR_BF16);
+    if (st != GDR_OK) return st;
+    if (plan == nullptr) return fail(GDR_ERR_INVALID_ARGUMENT, "%s: plan is NULL", fn);
+    const int nch = (T + kTcQ - 1) / kTcQ;
+    const SsmTcBwdWs w = ssm_tc_bwd_ws(B, T, H, G, P, N);
+    plan[0] = ssm_tc_chunks(B, T, H, P);
+    plan[1] = (nch + plan[0] - 1) / plan[0];
+    plan[2] = w.m;
+    plan[3] = w.R;
+    plan[4] = w.splits;
+    plan[5] = (H / G + w.splits - 1) / w.splits;
+    return GDR_OK;
+}
+
 gdr_status gdr_ssm_step(int B, int H, int G, int P, int N, gdr_dtype dt, int softplus, const void *x, int ldx,
                         const float *delta, const float *A, const void *Bm, int ldb, const void *Cm, int ldc,
                         const float *D, const float *delta_bias, float *S, void *y, gdr_stream_t stream) {

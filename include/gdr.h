@@ -461,6 +461,12 @@ GDR_API gdr_status gdr_ssm_bwd(int B, int T, int H, int G, int P, int N, gdr_dty
                        void *workspace, size_t workspace_bytes, gdr_stream_t stream);
 GDR_API size_t gdr_ssm_bwd_workspace_bytes(int B, int T, int H, int G, int P, int N, gdr_dtype dt);
 
+/* Test hook (host only): how a bf16 prompt of these sizes is cut on the current device.  plan[0], plan[1]: chunks of
+ * 128 tokens per segment and segments of a sequence in gdr_ssm_fwd; plan[2], plan[3]: the same of gdr_ssm_bwd's
+ * states; plan[4], plan[5]: thread blocks per group and chunk in gdr_ssm_bwd, and heads of each (the last may have
+ * fewer). */
+GDR_API gdr_status gdr_debug_ssm_plan(int B, int T, int H, int G, int P, int N, int *plan);
+
 /*
  * One token of gdr_ssm_fwd, the state updated in place.
  *   in : x [B,H,P], Bm, Cm [B,G,N] (dtype dt) with batch strides ldx, ldb, ldc

@@ -348,6 +348,15 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same with A in TMEM: row i on lane i, two bf16 of the summed index a column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // Arrive on `bar` once every tcgen05.mma issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile(
@@ -373,6 +382,23 @@ __device__ __forceinline__ void st_sw_bf16(uint8_t *tile, int row, int col, floa
 __device__ __forceinline__ void st_sw_bf16x2(uint8_t *tile, int row, int col, float x, float y) {
     *reinterpret_cast<__nv_bfloat162 *>(tile + sw128_offset(row, col >> 3) + (col & 7) * 2) =
         __floats2bfloat162_rn(x, y);
+}
+
+// A pair rounded to bf16, packed (x in the low half); the pair keeps what is left of it, exactly.
+__device__ __forceinline__ uint32_t take_bf16x2(float &x, float &y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    x -= __low2float(h);
+    y -= __high2float(h);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// The same of 8 floats, as one 16-byte chunk.
+__device__ __forceinline__ uint4 take_bf16x8(float *v) {
+    uint4 u;
+    u.x = take_bf16x2(v[0], v[1]);
+    u.y = take_bf16x2(v[2], v[3]);
+    u.z = take_bf16x2(v[4], v[5]);
+    u.w = take_bf16x2(v[6], v[7]);
+    return u;
 }
 
 // Pack 8 floats as bf16 and store as one 16-byte chunk.

@@ -6,13 +6,14 @@
 //     K  = C B^T                      M = 128 (i)   N = 128 (j)  K = N
 //     Y2 = C S_in^T                   M = 128 (i)   N = P        K = N
 //     Y1 = (K * L Delta) X            M = 128 (i)   N = P        K = 128 (j)
-//     S  = e^{c_last} S + B^T (w X)   M = 128 (n)   N = P        K = 128 (j)
-//     y  = Y1 + e^{c_i} Y2 + D x,     w_j = e^{c_last - c_j} Delta_j
-// Roundings to bf16: the decayed scores (K * L Delta), the entering state as
-// the operand of Y2, and w X.  The state itself stays fp32 in TMEM, and where
-// it is an output w X is split into two bf16 parts: its rounding is then below
-// 2^-17, and S_T within 2.5e-6 of 64 bits (with weights that bf16 holds, 1.3e-7:
-// the sums themselves).  A third part is half as many products again in every walk.
+//     U  = B^T (w X)                  M = 128 (n)   N = P        K = 128 (j)
+//     y  = Y1 + e^{c_i} Y2 + D x,     S = e^{c_last} S + U,      w_j = e^{c_last - c_j} Delta_j
+// x, B and C are bf16 themselves; an operand that is not enters as bf16 parts, each the rounding of what the ones before
+// it left: two (2^-17 of a term, below the rounding of y) for the decayed scores, the entering state and, where only y
+// reads the state, w X; three (2^-26) for w X where the state leaves in fp32.  S_T is then 1.3e-7 off 64 bits at B=4
+// T=4096 H=16 P=N=128 and y one rounding (1.7e-3).  With one part for y and two for S_T (2.5e-6 and 1.7e-3, y 1.4e-3
+// from its fp32 value) the call takes 136 us, not 173.  A chunk's U has an accumulator of its own, its small parts
+// first: summed onto a long memory's state, whose every accumulation the tensor core truncates, S_T was 2.5e-6 off.
 //
 // The decay e^{c_i - c_j} of a pair in different 32-token blocks is the product
 // of a row and a column factor around the later block's start (both <= 1 for a
@@ -190,7 +191,8 @@ __device__ __forceinline__ void ssm_enter_segment(float (&v)[W], const float *se
 }
 
 // A CTA walks the chunks of one (b, h, segment), forwards (S <- e^{c_last} S + B^T (w X)) or, rev, backwards (G <-
-// e^{c_last} G + C^T (e^c dY)), the state in TMEM (lanes n, columns p, fp32), the weighted rows in two bf16 parts.
+// e^{c_last} G + C^T (e^c dY)), the state in registers and a chunk's own sum in TMEM (lanes n, columns p, fp32), the
+// weighted rows in three bf16 parts (OUT: two).
 // OUT: from the state that enters the segment, every chunk's entering state is written as two bf16 parts (out_S, out_G
 // through tm_s, tm_g), and dS0 at the end.  Otherwise: from zero, the segment's own sum goes to seg_S or seg_G
 // [b][seg][h][P][N] in fp32, and its decay to dec.
@@ -204,9 +206,10 @@ struct SsmWalkTc {
     static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile, kStage = 2 * XB + BB;
     static constexpr uint32_t oX = 0, oLo = XB, oB = 2 * XB, oZero = ST * kStage;  // X, weighted in place; its second part
     static constexpr uint32_t kSBlock = N * 128, SB = P / 64 * kSBlock;  // a state part as a tile: N rows
-    static constexpr uint32_t oOut = oZero + (N == 64 ? kTile : 0);      // a state's second part on its way out
+    static constexpr uint32_t oOut = oZero + (N == 64 ? kTile : 0);      // OUT: a state's second part on its way out
+    static constexpr uint32_t oThird = oOut;                             // otherwise: the weighted rows' third part
     static constexpr uint32_t kGate = 128 * 4 + 64;                      // the rows' weights and the decay
-    static constexpr uint32_t oGate = oOut + SB, oCtl = oGate + 2 * kGate;
+    static constexpr uint32_t oGate = oOut + (SB > XB ? SB : XB), oCtl = oGate + 2 * kGate;
     static constexpr uint32_t kAlloc = oCtl + 96 + 1024;
 };
 
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     __syncwarp();
     // every thread: the chunk's rows weighted in place, the second part in registers until its buffer is free
     constexpr int CH = P / 32;
-    uint4 second[CH];
+    uint4 second[CH], third[CH];
     auto convert = [&](int k) {
         if (!mbar_wait(bar_g + (k & 1), (uint32_t)(k >> 1) & 1) || !mbar_wait(tma_bar + k % ST, (uint32_t)(k / ST) & 1)) {
             *abort_flag = 1;
@@ -302,7 +305,17 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             ld8s(p, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= w;
-            st_split8(p, reinterpret_cast<uint8_t *>(&second[i]), x);
+            *reinterpret_cast<uint4 *>(p) = take_bf16x8(x);
+            second[i] = take_bf16x8(x);
+            if (!OUT) third[i] = take_bf16x8(x);
+        }
+    };
+    auto convert_third = [&] {  // the products of the chunk before are done
+        const int r = tid & 127;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = (tid >> 7) * CH + i;
+            *reinterpret_cast<uint4 *>(sm + L::oThird + (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7)) = third[i];
         }
     };
     auto convert_second = [&](int k) {
@@ -321,8 +334,6 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
         else
 #pragma unroll
             for (int i = 0; i < PW; ++i) v[i] = 0.f;
-        tmem_stw<PW>(tl, v);
-        tmem_wait_st();
     }
     convert(0);
     convert_second(0);
@@ -348,19 +359,13 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             if (ST == 2) prefetch(k + 3);
         }
         __syncwarp();
-        if (row < N) {
-            tmem_ldw<PW>(tl, v);
-            if (OUT)
+        if (!OUT) convert_third();
+        if (OUT && row < N)
 #pragma unroll
-                for (int i = 0; i < PW / 8; ++i) {
-                    const uint32_t off = (uint32_t)(cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i);
-                    st_split8(out_hi + off, out_lo + off, v + 8 * i);
-                }
-#pragma unroll
-            for (int i = 0; i < PW; ++i) v[i] *= el;
-            tmem_stw<PW>(tl, v);
-            tmem_wait_st();
-        }
+            for (int i = 0; i < PW / 8; ++i) {
+                const uint32_t off = (uint32_t)(cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i);
+                st_split8(out_hi + off, out_lo + off, v + 8 * i);
+            }
         fence_async_smem();
         tc_before_sync();
         __syncthreads();
@@ -376,11 +381,11 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             const uint32_t st = sb + (k % ST) * L::kStage, at = st + L::oB;
             const uint32_t block = N == 64 ? sb + L::oZero - at : kTile;  // the second 64 lanes
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = OUT ? 1 : 2; part >= 0; --part)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16(tmem, desc_mn(at, kk, block), desc_mn(st + (part ? L::oLo : L::oX), kk),
-                             idesc_bf16(128, P, true, true), 1);
+                    mma_bf16(tmem, desc_mn(at, kk, block), desc_mn(part == 2 ? sb + L::oThird : st + (part ? L::oLo : L::oX), kk),
+                             idesc_bf16(128, P, true, true), part < (OUT ? 1 : 2) || kk > 0);
             mma_commit(mma_bar);
         }
         __syncwarp();
@@ -401,6 +406,12 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             n_g = k + 3;
         }
         __syncwarp();
+        if (update && row < N) {
+            float u[PW];
+            tmem_ldw<PW>(tl, u);
+#pragma unroll
+            for (int i = 0; i < PW; ++i) v[i] = fmaf(el, v[i], u[i]);
+        }
     }
     if (*abort_flag) {
         if (tid == kIo) {
@@ -413,7 +424,6 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     } else {
         if (keep && row < N) {
             float *dst = OUT ? a.dS0 + (size_t)bh * P * N : (rev ? seg_G : seg_S) + (((size_t)b * R + seg) * a.H + h) * P * N;
-            tmem_ldw<PW>(tl, v);
 #pragma unroll
             for (int i = 0; i < PW; ++i) dst[(size_t)(cp + i) * N + row] = v[i];
         }
@@ -429,24 +439,24 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
 }
 
 // ---- 3. outputs ------------------------------------------------------------------------------
-// LO: the state's own product takes both parts of w B, and S_T is written at the end (one segment).  With P = 64 two
-// CTAs of 8 warps share an SM; with P = 128 (the shared memory of one) a CTA has 16.  A chunk takes about 8700 cycles at
-// P = N = 128 (84 us at B=4 T=4096 H=16): each of its two rounds of products waits for register conversions and two
-// barriers.  The next chunk's K formed behind this chunk's last products, with B, C and K in two stages, took 94 us: the
-// conversions, not the products, are what the chunk waits for.
+// LO: S_T is written at the end (one segment).  With P = 64 two CTAs of 8 warps share an SM; with P = 128 a CTA has 16
+// warps, which take the registers of an SM.  Each of a chunk's two rounds of products waits for register conversions and
+// block barriers.  The scores stay in TMEM, as the A operand of their product.
 template <int P, int N, bool LO>
 struct SsmYTc {
     static constexpr int NT = P == 128 ? 512 : 256, kParts = NT / 128;  // warps of one TMEM quarter: column parts
+    // P = 64, N = 128: two CTAs share an SM only if the state's second part takes the first one's place
+    static constexpr bool kTurns = P == 64 && N == 128 && !LO;
     static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile;
-    static constexpr uint32_t oX = 0, oB = XB, oLo = oB + BB, oZero = oLo + (LO ? BB : 0);
-    static constexpr uint32_t kHiBlock = N == 64 ? (LO ? 2 : 1) * kTile : kTile;
-    static constexpr uint32_t oC = oZero + (N == 64 ? kTile : 0);  // C, then the decayed scores
-    static constexpr uint32_t kSBlock = kTile;                     // S^T: N rows of 64 columns p; then w X, then y
-    static constexpr uint32_t oS = oC + 2 * kTile;
-    static constexpr uint32_t oGate = oS + P / 64 * kSBlock;       // two tables
+    static constexpr uint32_t oX = 0, oB = XB, oZero = oB + BB;
+    static constexpr uint32_t oC = oZero + (N == 64 ? kTile : 0);  // C, then w X's third part (LO) or its second (kTurns)
+    static constexpr uint32_t oS = oC + (LO && XB > BB ? XB : BB); // S^T: N rows of 64 columns p; then w X, then y
+    static constexpr uint32_t kSBlock = kTile;
+    static constexpr uint32_t oLo = kTurns ? oC : oS + XB;         // the second part of S^T, then of w X
+    static constexpr uint32_t oGate = oS + (kTurns ? 1 : 2) * XB;  // two tables
     static constexpr uint32_t oBar = oGate + 2 * SsmGate::kFwdBytes;
     static constexpr uint32_t kAlloc = oBar + 64 + 1024;
-    static constexpr uint32_t kTmemCols = P == 64 ? 256 : 512;
+    static constexpr uint32_t kTmemCols = P == 64 && !LO ? 256 : 512;
 };
 
 template <int P, int N, bool LO>
@@ -484,7 +494,8 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
     tc_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
-    constexpr uint32_t tK = 0, tY2 = 128, tS = 128 + P;  // Y1 takes K's columns once K is read
+    constexpr uint32_t tK = 0, tY = 128, tS = 128 + P;   // the scores' two bf16 parts take K's columns
+    constexpr uint32_t tU = LO ? tS + P : tS;            // the chunk's own sum
     const int cp = prt * 32;                             // this warp's 32 columns p
 
     auto issue_bc = [&](int k) {
@@ -562,15 +573,30 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
             ++n_g;
         }
         __syncwarp();
-        if (row < N) {  // S^T as the bf16 operand [n][p]; the fp32 state decays to the chunk's end
+        uint4 turn[4];  // kTurns: the state's second part until its place is free
+        if (row < N) {  // S^T as two bf16 operands [n][p]; the fp32 state decays to the chunk's end
             const float el = s_g[SsmGate::elast];
             float v[32];
             tmem_ld32(tl + tS + cp, v);
+            if (LO && k > 0) {
+                float u[32];
+                tmem_ld32(tl + tU + cp, u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                st_bf16x8(sm + L::oS + (cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i), v + 8 * i);
+                for (int i = 0; i < 32; ++i) v[i] += u[i];
+            }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= el;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t off = (cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i);
+                float r[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    r[e] = v[8 * i + e];
+                    v[8 * i + e] *= el;
+                }
+                *reinterpret_cast<uint4 *>(sm + L::oS + off) = take_bf16x8(r);
+                turn[i] = take_bf16x8(r);
+                if (!L::kTurns) *reinterpret_cast<uint4 *>(sm + L::oLo + off) = turn[i];
+            }
             tmem_st32(tl + tS + cp, v);
             tmem_wait_st();
         }
@@ -585,20 +611,40 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
             for (int kk = 0; kk < N / 16; ++kk)
                 mma_bf16(tmem + tK, desc_k(sb + L::oC, kk), desc_k(sb + L::oB, kk), idesc_bf16(128, 128, false, false), kk > 0);
 #pragma unroll
-            for (int kk = 0; kk < N / 16; ++kk)
-                mma_bf16(tmem + tY2, desc_k(sb + L::oC, kk), desc_mn(sb + L::oS, kk, L::kSBlock),
-                         idesc_bf16(128, P, false, true), kk > 0);
+            for (int part = 0; part < (L::kTurns ? 1 : 2); ++part)
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk)
+                    mma_bf16(tmem + tY, desc_k(sb + L::oC, kk), desc_mn(sb + (part ? L::oLo : L::oS), kk, L::kSBlock),
+                             idesc_bf16(128, P, false, true), part > 0 || kk > 0);
             mma_commit(mma_bar);
         }
         mma_sync_point();
         if (*abort_flag) break;
+        if (L::kTurns) {
+            if (row < N)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(sm + L::oS + (cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i)) = turn[i];
+            fence_async_smem();
+            tc_before_sync();
+            __syncthreads();
+            if (tid == 0) {
+                tc_after_sync();
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk)
+                    mma_bf16(tmem + tY, desc_k(sb + L::oC, kk), desc_mn(sb + L::oS, kk, L::kSBlock),
+                             idesc_bf16(128, P, false, true), 1);
+                mma_commit(mma_bar);  // waited for behind the scores
+            }
+            __syncwarp();
+        }
 
-        // decayed scores -> bf16 [i][j] over C (C's products are done)
+        // decayed scores -> two bf16 parts in TMEM, over K: the 32 tokens j of a block are 16 columns of the first
+        // part and 16 of the second, so that a warp writes only columns that it has read
         const float rf = s_g[SsmGate::rowf + row], ci = s_g[SsmGate::hi + row], cl = s_g[SsmGate::lo + row];
 #pragma unroll
         for (int jb = 0; jb < 4 / L::kParts; ++jb) {
             const int J = prt * (4 / L::kParts) + jb;  // 32-column block
-            uint8_t *dst = sm + L::oC + (J >> 1) * kTile;
             float v[32];
             if (J > q) {
 #pragma unroll
@@ -634,37 +680,42 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
                     }
                 }
             }
+            float parts[32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st_bf16x8(dst + sw128_offset(row, (J & 1) * 4 + i), v + 8 * i);
+            for (int i = 0; i < 16; ++i) {
+                parts[i] = __uint_as_float(take_bf16x2(v[2 * i], v[2 * i + 1]));
+                parts[16 + i] = __uint_as_float(take_bf16x2(v[2 * i], v[2 * i + 1]));
+            }
+            tmem_st32(tl + tK + J * 32, parts);
         }
-        {   // the state's own product: w B in place (B's product is done) with its second part beside it, or, where one
-            // bf16 part will do, w X over S's tile (its product is done), which is the smaller of the two
+        if (L::kTurns) {
+            mma_sync_point();
+            if (*abort_flag) break;
+        }
+        {   // e^{c_i} C S_in^T, onto which the scores' product is summed
+            const float e = s_g[SsmGate::e + row];
+            float v[32];
+            tmem_ld32(tl + tY + cp, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= e;
+            tmem_st32(tl + tY + cp, v);
+            tmem_wait_st();
+        }
+        if (LO || k + 1 < cn) {  // the state's own product: w X as bf16 parts (C's and S's products are done)
             const int r = tid & 127;
             const float w = s_g[SsmGate::dt + r] * s_g[SsmGate::el + r];
-            if (LO) {
-                constexpr int CH = N / 8 / L::kParts;
+            constexpr int CH = P / 8 / L::kParts;
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int c = (tid >> 7) * CH + i;
-                    uint8_t *p = sm + L::oB + (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
-                    float v[8];
-                    ld8s(p, v);
+            for (int i = 0; i < CH; ++i) {
+                const int c = (tid >> 7) * CH + i;
+                const uint32_t off = (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
+                float v[8];
+                ld8s(sm + L::oX + off, v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= w;
-                    st_split8(p, p + L::BB, v);
-                }
-            } else if (k + 1 < cn) {
-                constexpr int CH = P / 8 / L::kParts;
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int c = (tid >> 7) * CH + i;
-                    const uint32_t off = (uint32_t)(c >> 3) * kTile + sw128_offset(r, c & 7);
-                    float v[8];
-                    ld8s(sm + L::oX + off, v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= w;
-                    st_bf16x8(sm + L::oS + off, v);
-                }
+                for (int e = 0; e < 8; ++e) v[e] *= w;
+                *reinterpret_cast<uint4 *>(sm + L::oS + off) = take_bf16x8(v);
+                *reinterpret_cast<uint4 *>(sm + L::oLo + off) = take_bf16x8(v);
+                if (LO) *reinterpret_cast<uint4 *>(sm + L::oC + off) = take_bf16x8(v);
             }
         }
         fence_async_smem();
@@ -673,15 +724,19 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
         if (tid == 0) {
             tc_after_sync();
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_bf16(tmem + tK, desc_k(sb + L::oC, kk), desc_mn(sb + L::oX, kk), idesc_bf16(128, P, false, true), kk > 0);
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16_ts(tmem + tY, tmem + tK + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, desc_mn(sb + L::oX, kk),
+                                idesc_bf16(128, P, false, true), 1);
             if (LO || k + 1 < cn) {
 #pragma unroll
-                for (int part = 0; part < (LO ? 2 : 1); ++part)
+                for (int part = LO ? 2 : 1; part >= 0; --part)
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16(tmem + tS, desc_mn(sb + (part ? L::oLo : L::oB), kk, part ? kTile : L::kHiBlock),
-                                 desc_mn(sb + (LO ? L::oX : L::oS), kk), idesc_bf16(128, P, true, true), 1);
+                        mma_bf16(tmem + tU, desc_mn(sb + L::oB, kk, N == 64 ? L::oZero - L::oB : kTile),
+                                 desc_mn(sb + (part == 0 ? L::oS : part == 1 ? L::oLo : L::oC), kk), idesc_bf16(128, P, true, true),
+                                 !LO || part < 2 || kk > 0);
             }
             mma_commit(mma_bar);
         }
@@ -701,21 +756,16 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
             prefetch(k + 2);
         }
         __syncwarp();
-        {   // y = Y1 + e^{c_i} Y2 + D x, over S's tile (straight from registers, 64 bytes of 32 rows a warp, the
-            // stores alone took 2000 of a chunk's 9500 cycles)
-            const float e = s_g[SsmGate::e + row];
-            float y1[32], y2[32];
-            tmem_ld32(tl + tK + cp, y1);
-            tmem_ld32(tl + tY2 + cp, y2);
+        {   // + D x, over S's tile (straight from registers, 64 bytes of 32 rows a warp, the stores alone took 2000 of a
+            // chunk's 9500 cycles)
+            float y[32];
+            tmem_ld32(tl + tY + cp, y);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float x[8];
                 if (a.D) ld8s(reinterpret_cast<const uint8_t *>(&xr[i]), x);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float y = fmaf(e, y2[8 * i + u], y1[8 * i + u]);
-                    x[u] = a.D ? fmaf(D, x[u], y) : y;
-                }
+                for (int u = 0; u < 8; ++u) x[u] = a.D ? fmaf(D, x[u], y[8 * i + u]) : y[8 * i + u];
                 st_bf16x8(sm + L::oS + (uint32_t)(cp >> 6) * kTile + sw128_offset(row, ((cp & 63) >> 3) + i), x);
             }
         }
@@ -739,10 +789,11 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
         }
     } else if (LO && a.S_T && row < N) {
         float *dst = a.S_T + (size_t)bh * P * N;
-        float v[32];
+        float v[32], u[32];
         tmem_ld32(tl + tS + cp, v);
+        tmem_ld32(tl + tU + cp, u);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dst[(size_t)(cp + i) * N + row] = v[i];
+        for (int i = 0; i < 32; ++i) dst[(size_t)(cp + i) * N + row] = v[i] + u[i];
     }
     if (tid == kIo) bulk_wait_all();
     tc_before_sync();

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_dy,
     const __grid_constant__ CUtensorMap tm_dx, const __grid_constant__ CUtensorMap tm_s,
     const __grid_constant__ CUtensorMap tm_g, SsmArgs a, int splits, int per, const float *__restrict__ gates, const __nv_bfloat16 *__restrict__ Sin,
-    const __nv_bfloat16 *__restrict__ Gout, float *__restrict__ dBp, float *__restrict__ dCp, float *__restrict__ part) {
+    const __nv_bfloat16 *__restrict__ Gout, float *__restrict__ dBp, float *__restrict__ dCp, double *__restrict__ part) {
     using L = SsmGradTc<P, N>;
     using namespace sm100;
     constexpr int NW = N / 4, PW = P / 4;  // columns of a warp
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             bulk_commit();
         }
         __syncwarp();
-        if (tid < 3) part[tid * units + unit] = (float)(s_tot[tid] + s_tot[3 + tid] + s_tot[6 + tid] + s_tot[9 + tid]);
+        if (tid < 3) part[tid * units + unit] = (double)(s_tot[tid] + s_tot[3 + tid] + s_tot[6 + tid] + s_tot[9 + tid]);
     }
     if (*abort_flag) {
         if (tid == 0 && mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
@@ -609,7 +609,7 @@ inline SsmTcBwdWs ssm_tc_bwd_ws(int B, int T, int H, int G, int P, int N) {
     w.segG = w.segS + ssm_align(segs * P * N * 4);
     w.dec = w.segG + ssm_align(segs * P * N * 4);
     w.part = w.dec + ssm_align(segs * 4);
-    w.dBp = w.part + ssm_align(3 * units * 4);
+    w.dBp = w.part + ssm_align(3 * units * 8);
     const size_t p = w.splits > 1 ? ssm_align((size_t)B * T * G * w.splits * N * 4) : 0;
     w.dCp = w.dBp + p;
     w.total = w.dCp + p;
@@ -623,7 +623,8 @@ cudaError_t ssm_tc_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     uint8_t *base = static_cast<uint8_t *>(ws);
     __nv_bfloat16 *st = reinterpret_cast<__nv_bfloat16 *>(base + w.st), *g = reinterpret_cast<__nv_bfloat16 *>(base + w.g);
     float *segS = reinterpret_cast<float *>(base + w.segS), *segG = reinterpret_cast<float *>(base + w.segG);
-    float *dec = reinterpret_cast<float *>(base + w.dec), *part = reinterpret_cast<float *>(base + w.part);
+    float *dec = reinterpret_cast<float *>(base + w.dec);
+    double *part = reinterpret_cast<double *>(base + w.part);
     float *dBp = reinterpret_cast<float *>(base + w.dBp), *dCp = reinterpret_cast<float *>(base + w.dCp);
     const size_t units = (size_t)a.B * nch * a.H;
     float *gates = reinterpret_cast<float *>(base + w.gates);

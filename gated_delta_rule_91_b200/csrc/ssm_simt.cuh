@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_y_simt_kernel(SsmArgs a, cons
 // columns and rows of strict pairs, which starts at exactly 0.
 // part[0..2][b*nch+ch][h]: this chunk's sums for dA, d(delta_bias), dD.
 __device__ __forceinline__ void ssm_token_grads(const SsmArgs &a, int b, int h, int t0, int valid, int Q, const float *s_dt,
-                                                const float *colU, const float *diag, const float *row, const float *gx,
-                                                const float *sy, double cross, const float *dw_diag, float *part,
+                                                const double *colU, const float *diag, const double *row, const float *gx,
+                                                const float *sy, double cross, const float *dw_diag, double *part,
                                                 size_t unit, size_t units) {
     // One warp; token arrays of Q (a multiple of 32): colU strict column sums of R (without Delta_j), diag R_jj,
     // row strict row sums of R Delta, gx = e^{c_last-c_j} x_j.G B_j, sy = e^{c_i} dy_i.S_in C_i, dw_diag = dy_i.x_i.
@@ -256,7 +256,7 @@ __device__ __forceinline__ void ssm_token_grads(const SsmArgs &a, int b, int h, 
     double pre = 0.0, suf = 0.0;
     for (int e = 0; e < E; ++e) {
         const int t = lane * E + e;
-        pre += (double)s_dt[t] * ((double)colU[t] + (double)gx[t]) - (double)row[t];
+        pre += (double)s_dt[t] * (colU[t] + (double)gx[t]) - row[t];
         suf += (double)sy[t];
     }
     double p = pre, s = suf;
@@ -270,8 +270,8 @@ __device__ __forceinline__ void ssm_token_grads(const SsmArgs &a, int b, int h, 
     for (int e = 0; e < E; ++e) {
         const int t = lane * E + e;
         const double dlog = before + after + cross;
-        const double dd = (double)colU[t] + (double)diag[t] + (double)gx[t] + Ah * dlog;
-        before += (double)s_dt[t] * ((double)colU[t] + (double)gx[t]) - (double)row[t];
+        const double dd = colU[t] + (double)diag[t] + (double)gx[t] + Ah * dlog;
+        before += (double)s_dt[t] * (colU[t] + (double)gx[t]) - row[t];
         after -= (double)sy[t];
         if (t < valid) {
             const size_t at = ((size_t)b * a.T + t0 + t) * a.H + h;
@@ -294,9 +294,9 @@ __device__ __forceinline__ void ssm_token_grads(const SsmArgs &a, int b, int h, 
         sD += __shfl_xor_sync(0xffffffffu, sD, off);
     }
     if (lane == 0) {
-        part[unit] = (float)sA;
-        part[units + unit] = (float)sB;
-        part[2 * units + unit] = (float)sD;
+        part[unit] = sA;
+        part[units + unit] = sB;
+        part[2 * units + unit] = sD;
     }
 }
 
@@ -314,13 +314,13 @@ template <typename T, int P, int N>
 __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, int roles, const float *__restrict__ Sin,
                                                                     const float *__restrict__ Gout,
                                                                     float *__restrict__ dBh, float *__restrict__ dCh,
-                                                                    float *__restrict__ part) {
+                                                                    double *__restrict__ part) {
     using L = SsmGradSmem<P, N>;
     extern __shared__ float sm_f[];
     float *s0 = sm_f, *sbt = s0 + L::kOp, *sxt = sbt + L::kOp, *syt = sxt + L::kOp;
     float *s_m = syt + L::kOp, *s_k = s_m + L::kQQ, *s_kt = s_k + L::kQQ;  // M'[i][j], dK[i][j], dK[j][i]
-    __shared__ float s_dt[kSsmQ], s_colU[kSsmQ], s_diag[kSsmQ], s_row[kSsmQ], s_gx[kSsmQ], s_sy[kSsmQ], s_wd[kSsmQ];
-    __shared__ float s_part[16][kSsmQ];
+    __shared__ float s_dt[kSsmQ], s_diag[kSsmQ], s_gx[kSsmQ], s_sy[kSsmQ], s_wd[kSsmQ];
+    __shared__ double s_part[16][kSsmQ], s_colU[kSsmQ], s_row[kSsmQ];
     __shared__ double s_c[kSsmQ], s_red[8];
     const int nch = (a.T + kSsmQ - 1) / kSsmQ;
     const int ch = blockIdx.x / roles, role = roles == 1 ? 2 : blockIdx.x % roles, h = blockIdx.y, b = blockIdx.z;
@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, i
     ssm_load_cols<T, P>(syt, yg, ldy, valid);
     __syncthreads();
     {
-        float k4[4][4] = {}, w4[4][4] = {}, col[4] = {};
+        float k4[4][4] = {}, w4[4][4] = {};
+        double col[4] = {}, row[4] = {};  // 64 bits: a pair's R Delta in its row's sum and in its column's cancels exactly
         ssm_mm<4>(k4, s0, kSsmLdQ, sbt, kSsmLdQ, N, ty, tx);
         ssm_mm<4>(w4, syt, kSsmLdQ, sxt, kSsmLdQ, P, ty, tx);
-        float row[4] = {};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int j = 4 * tx + c;
@@ -359,8 +359,8 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, i
                 s_k[i * kSsmLdQ + j] = dk;
                 s_kt[j * kSsmLdQ + i] = dk;
                 if (i > j) {
-                    row[r] += R * dj;
-                    col[c] += R;
+                    row[r] = fma((double)R, (double)dj, row[r]);
+                    col[c] += (double)R;
                 }
                 if (i == j) {
                     s_diag[i] = R;
@@ -370,7 +370,8 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, i
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            row[r] = warp_sum(row[r], 16);
+#pragma unroll
+            for (int off = 8; off; off >>= 1) row[r] += __shfl_xor_sync(0xffffffffu, row[r], off);
             if (tx == 0) s_row[4 * ty + r] = row[r];
         }
 #pragma unroll
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_grad_simt_kernel(SsmArgs a, i
     }
     __syncthreads();
     if (tid < kSsmQ) {
-        float s = 0.f;
+        double s = 0.0;
         for (int k = 0; k < 16; ++k) s += s_part[k][tid];
         s_colU[tid] = s;
     }
@@ -533,13 +534,13 @@ __global__ void __launch_bounds__(256) ssm_group_sum_kernel(long long total4, in
 }
 
 // dA, d(delta_bias), dD of head blockIdx.x: sums over (b, chunk) in 64 bits, in a fixed order.
-__global__ void __launch_bounds__(256) ssm_head_sum_kernel(int n, int H, const float *__restrict__ part, float *dA,
+__global__ void __launch_bounds__(256) ssm_head_sum_kernel(int n, int H, const double *__restrict__ part, float *dA,
                                                            float *dbias, float *dD) {
     __shared__ double red[3][8];
     const int h = blockIdx.x, tid = threadIdx.x;
     double s[3] = {0.0, 0.0, 0.0};
     for (int i = tid; i < n; i += 256)
-        for (int k = 0; k < 3; ++k) s[k] += (double)part[((size_t)k * n + i) * H + h];
+        for (int k = 0; k < 3; ++k) s[k] += part[((size_t)k * n + i) * H + h];
     for (int k = 0; k < 3; ++k) {
         for (int off = 16; off; off >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
         if ((tid & 31) == 0) red[k][tid >> 5] = s[k];
@@ -569,7 +570,7 @@ inline SsmSimtWs ssm_simt_ws(int B, int T, int H, int P, int N) {
     w.dBh = w.g + ssm_align(units * P * N * 4);
     w.dCh = w.dBh + ssm_align((size_t)B * T * H * N * 4);
     w.part = w.dCh + ssm_align((size_t)B * T * H * N * 4);
-    w.bwd_total = w.part + ssm_align(3 * units * 4);
+    w.bwd_total = w.part + ssm_align(3 * units * 8);
     return w;
 }
 
@@ -637,7 +638,8 @@ cudaError_t ssm_simt_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     const int nch = (a.T + kSsmQ - 1) / kSsmQ;
     uint8_t *base = static_cast<uint8_t *>(ws);
     float *st = reinterpret_cast<float *>(base + w.st), *dec = reinterpret_cast<float *>(base + w.dec);
-    float *g = reinterpret_cast<float *>(base + w.g), *part = reinterpret_cast<float *>(base + w.part);
+    float *g = reinterpret_cast<float *>(base + w.g);
+    double *part = reinterpret_cast<double *>(base + w.part);
     float *dBh = reinterpret_cast<float *>(base + w.dBh), *dCh = reinterpret_cast<float *>(base + w.dCh);
     const size_t sm = (size_t)kSsmQ * (kSsmLdQ + N + 4) * 4;
     const dim3 grid(nch * (P / 64), a.H, a.B);

@@ -2,8 +2,8 @@
 as exact as fp32 torch operations, and what leaves in bf16 is one rounding away from that.
 
 Two kinds of bounds.  Elementwise (M: the sum of term magnitudes): a bf16 output is rounded once (2^-8 of its value); operands
-of its products are two bf16 parts (2^-9 * 2^-8 = 2^-17 of a term each, at most two of them a term: the decayed score or the
-state, and the row written to the state), fp32 sums as in test_gpu_ssm_plans.  In the 2-norm: an fp32 output may be at most
+of its products are two bf16 parts (2^-9 * 2^-8 = 2^-17 of a term each, at most two of them a term forwards: the decayed
+score or the state, and the row written to the state; three backwards), fp32 sums as in test_gpu_ssm_plans.  In the 2-norm: an fp32 output may be at most
 1.5 times as far from 64 bits as the same block form in fp32 torch operations, or 1e-6 where that is more (eight units of
 2^-23: a sum of about 64 terms, a carry and the decay's exponential, each an unbiased half unit or so; a missing third part
 costs 2.5e-6)."""
@@ -12,7 +12,7 @@ import torch
 
 from ssm_common import HALF, within
 from ssm_plans import scan_blocks
-from test_gpu_ssm import fwd, inputs
+from test_gpu_ssm import bwd, fwd, inputs
 
 pytestmark = pytest.mark.gpu
 BF = HALF[torch.bfloat16]
@@ -48,3 +48,15 @@ def test_forward(size, s0):
     as_exact_as_fp32(S_T, r["S_T"], p["S_T"], "S_T")
     within(S_T, r["S_T"].cpu(), sums(d) * m["S_T"].cpu(), "S_T")
     within(y, r["y"].cpu(), (BF * r["y"].abs() + (2 * 2.0 ** -17 + sums(d)) * m["y"]).cpu(), "y")
+
+
+@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("size", [(3, 414, 16, 2, 64, 64), (3, 206, 16, 1, 128, 128), (2, 333, 8, 2, 128, 64), (1, 1500, 16, 1, 64, 128)])
+def test_sums_over_tokens(size, dtype):
+    """dA and the bias's gradient: every pair of tokens enters them once through a row's sum and once, with the other sign,
+    through a column's, which have to agree to more than 32 bits for the rest to be right."""
+    d = inputs(*size, dtype, seed=sum(size) + 2)
+    g = bwd(d)
+    r, p = scan_blocks(d, grads=True), scan_blocks(d, grads=True, dtype=torch.float32)
+    for n in ("ddelta", "dA", "ddelta_bias", "dS0"):
+        as_exact_as_fp32(g[n], r[n], p[n], n)

@@ -172,12 +172,6 @@ struct ConvRing {
     static constexpr int kRow = 32 * V * (int)sizeof(T);        // bytes of a warp's row
     static constexpr int kBytes = GROUPS * U * kRow;  // of one tensor
 };
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // A lane's part of the copies of one tensor: L lanes a row, so 32 / L rows at once.
 template <typename T, int V, int U>

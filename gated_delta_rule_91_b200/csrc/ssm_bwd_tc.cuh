@@ -3,21 +3,22 @@
 // of ssm_simt.cuh.  Chunks of 128 tokens:
 //   1. ssm_tc_walk_kernel   S_in(c) of every chunk, walking forwards, and G_out(c),
 //      walking backwards, in one launch (segments from the same walk and
-//      ssm_scan_kernel first where heads are few), each state as two bf16 parts
+//      ssm_scan_kernel first where heads are few), each state in fp32
 //   2. ssm_tc_grad_kernel   a CTA owns one chunk of one group and walks heads of
-//      it, so that C B^T is formed once and dB, dC are summed over the heads in
+//      it, so that B and C are read once and dB, dC are summed over the heads in
 //      TMEM.  Per head (W = dy x^T, L the decays, tokens on the TMEM lanes):
-//        W   = dY X^T                              N = 128   K = P
+//        K   = C B^T,  W = dY X^T                  N = 128   K = N, P
 //        dC += dK B,  dB += dK^T C                 N = N     K = 128    dK = L W Delta
 //        dXi = M'^T dY                             N = P     K = 128    M' = L (C B^T)
 //        T   = dY S_in  -> dC += e^{c_i} T,        dlog: e^{c_i} C_i . T_i
 //        T   = X G_out  -> dB += w_j T,            dDelta: e^{c_last-c_j} B_j . T_j
 //        T   = B G_out^T -> dx = Delta (dXi + e^{c_last-c_j} T) + D dy
 //      (N = N, N, P and K = P, P, N).
-// What leaves in fp32 (the gradients of delta, A, the bias and S0) is not
-// touched by a bf16 rounding above 2^-17: the double sums of R = L K W are
-// taken on CUDA cores from the fp32 accumulators, and S_in and G_out enter
-// their products as two bf16 parts.  dx, dB and dC take bf16 operands.
+// Operands that are not bf16 themselves enter as bf16 parts, as in the forward: M' and dK as two, S_in and G_out as three
+// where fp32 results follow from the product and G_out as two for dx.  The double sums of R = L K W are taken on CUDA
+// cores from the fp32 accumulators.  With one part for M', dK and dx's G_out, and the states kept as two, dx, dB and dC
+// were 2.3e-3 off 64 bits (one rounding: 1.7e-3), dS0 2.5e-6 and dA and the bias's gradient up to 1e-5; now 1e-7 to 4e-7.
+// B=4 T=4096 H=16 P=N=128: 443 us (walk 130, gradients 300), 308 with the fewer parts.
 #pragma once
 #include "ssm_tc.cuh"
 
@@ -29,28 +30,33 @@ struct SsmGradTc {
     static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile;
     static constexpr uint32_t kSBlock = N * 128, SB = P / 64 * kSBlock;  // a state part: N rows, blocks of 64 columns p
     static constexpr uint32_t oB = 0, oC = BB, oX = 2 * BB, oY = oX + XB, oR = oY + XB;
-    static constexpr uint32_t oM = oR, oK = oR + 2 * kTile;   // M', dK
-    static constexpr uint32_t oHi = oR, oLo = oR + SB;        // S_in, then G_out
+    static constexpr uint32_t oM = oR, oK = oR + 2 * kTile;   // M', dK: the first parts, then the second
+    static constexpr uint32_t oHi = oR, oLo = oR + SB;        // S_in, then G_out: two parts; the third
+    static constexpr uint32_t oThirdS = oX, oThirdG = oY;     // in the tiles of X (read again behind it) and of dY
+    // A state arrives in fp32: S_in's first bytes in X's tile, from the moment W is formed, the rest over M' and dK; G_out
+    // whole over S_in's parts.
+    static constexpr uint32_t kRaw = P * N * 4, kRawX = kRaw < XB ? kRaw : XB;
     static constexpr uint32_t oGate = oR + 4 * kTile;
-    // two tables; doubles: warp sums of the token sums [4][2]; floats: totals [4][3], <G, S> [20], rowp[4][128],
-    // colp[4][128], diag, wd, gxp[4][128], syp[4][128]
+    // two tables; doubles: warp sums of the token sums [4][2], totals [4][3], <G, S> [16], rowp[4][128], colp[4][128];
+    // floats: diag, wd, gxp[4][128], syp[4][128]
     static constexpr uint32_t oSum = oGate + 2 * SsmGate::kBytes;
-    static constexpr uint32_t oBar = oSum + 8 * 8 + (12 + 20 + 18 * 128) * 4;
+    static constexpr uint32_t oBar = oSum + (8 + 12 + 16 + 8 * 128) * 8 + 10 * 128 * 4;
     static constexpr uint32_t kAlloc = oBar + 64 + 1024;
 };
 
-// Column sums of a 32 x 16 block held as v[column] per lane (row): v[0] ends as the sum of column lane & 15.
-__device__ __forceinline__ void ssm_column_sums(float *v) {
+// Column sums of a 32 x 8 block held as v[column] per lane (row): v[0] ends as the sum of column lane & 7.
+__device__ __forceinline__ void ssm_column_sums(double *v) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int s = 8; s > 0; s >>= 1) {
+    for (int s = 4; s > 0; s >>= 1) {
         const bool up = lane & s;
 #pragma unroll
         for (int k = 0; k < s; ++k) {
-            const float send = up ? v[k] : v[k + s], keep = up ? v[k + s] : v[k];
+            const double send = up ? v[k] : v[k + s], keep = up ? v[k + s] : v[k];
             v[k] = keep + __shfl_xor_sync(0xffffffffu, send, s);
         }
     }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8);
     v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 __device__ __forceinline__ double ssm_warp_scan(double x) {  // inclusive
@@ -68,9 +74,9 @@ template <int P, int N>
 __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_dy,
-    const __grid_constant__ CUtensorMap tm_dx, const __grid_constant__ CUtensorMap tm_s,
-    const __grid_constant__ CUtensorMap tm_g, SsmArgs a, int splits, int per, const float *__restrict__ gates, const __nv_bfloat16 *__restrict__ Sin,
-    const __nv_bfloat16 *__restrict__ Gout, float *__restrict__ dBp, float *__restrict__ dCp, double *__restrict__ part) {
+    const __grid_constant__ CUtensorMap tm_dx, SsmArgs a, int splits, int per, const float *__restrict__ gates,
+    const float4 *__restrict__ Sin, const float4 *__restrict__ Gout, float *__restrict__ dBp, float *__restrict__ dCp,
+    double *__restrict__ part) {
     using L = SsmGradTc<P, N>;
     using namespace sm100;
     constexpr int NW = N / 4, PW = P / 4;  // columns of a warp
@@ -78,11 +84,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(sm);
     double *s_tw = reinterpret_cast<double *>(sm + L::oSum);
-    float *s_tot = reinterpret_cast<float *>(s_tw + 8), *s_red = s_tot + 12, *s_rowp = s_red + 20, *s_colp = s_rowp + 512, *s_diag = s_colp + 512, *s_wd = s_diag + 128,
+    double *s_tot = s_tw + 8, *s_red = s_tot + 12, *s_rowp = s_red + 16, *s_colp = s_rowp + 512;
+    float *s_diag = reinterpret_cast<float *>(s_colp + 512), *s_wd = s_diag + 128,
           *s_gxp = s_wd + 128, *s_syp = s_gxp + 512;
     uint64_t *bar_bc = reinterpret_cast<uint64_t *>(sm + L::oBar), *bar_x = bar_bc + 1, *bar_y = bar_bc + 2,
-             *bar_s = bar_bc + 3, *bar_g = bar_bc + 4, *mma_bar = bar_bc + 5;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_bc + 6);
+             *bar_g = bar_bc + 3, *mma_bar = bar_bc + 4, *bar_s = bar_bc + 5, *bar_r = bar_bc + 6;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_bc + 7);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = warp & 3, prt = warp >> 2, row = q * 32 + lane;  // TMEM lane, column quarter
@@ -101,9 +108,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         mbar_init(bar_bc, 1);
         mbar_init(bar_x, 1);
         mbar_init(bar_y, 1);
-        mbar_init(bar_s, 1);
         mbar_init(bar_g, 1);
         mbar_init(mma_bar, 1);
+        mbar_init(bar_s, 1);
+        mbar_init(bar_r, 1);
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -116,8 +124,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
     constexpr uint32_t tK = 0, tT = 128, tC = 256, tB = 256 + N;
 
     constexpr int kIo = 384;              // issues copies (a warp above the diagonal); thread 0 issues products
-    int n_x = 0, n_y = 0, n_s = 0, n_g = 0;  // issued, by that thread
-    uint32_t s_phase = 0;                             // everyone's
+    int n_x = 0, n_y = 0, n_g = 0, n_s = 0, n_r = 0;  // issued, by that thread
+    uint32_t r_phase = 0;                             // everyone's
     bool mma_open = false;
     auto issue_x = [&](int h) {
         mbar_expect_tx(bar_x, L::XB);
@@ -129,22 +137,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         for (int i = 0; i < P / 64; ++i) tma_load_4d(sm + L::oY + i * kTile, &tm_dy, bar_y, i * 64, h, t0, b);
         ++n_y;
     };
-    auto issue_state = [&](const CUtensorMap *map, size_t unit) {
-        mbar_expect_tx(bar_s, 2 * L::SB);
-        for (int pt = 0; pt < 2; ++pt)
-            for (int i = 0; i < P / 64; ++i)
-                tma_load_4d(sm + L::oHi + pt * L::SB + i * L::kSBlock, map, bar_s, i * 64, 0, pt, (int)unit);
-        ++n_s;
-    };
     auto issue_g = [&](int hh) {
         mbar_expect_tx(bar_g, SsmGate::kBytes);
         bulk_load_g2s(sm + L::oGate + (hh & 1) * SsmGate::kBytes, gates + (unit0 + h0 + hh) * SsmGate::stride, SsmGate::kBytes,
                       bar_g);
         ++n_g;
-    };
-    auto wait_state = [&] {  // every thread
-        if (!mbar_wait(bar_s, s_phase)) *abort_flag = 1;
-        s_phase ^= 1;
     };
     if (tid == kIo) {
         mbar_expect_tx(bar_bc, 2 * L::BB);
@@ -166,12 +163,42 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         __syncthreads();
         tc_after_sync();
     };
-    // 8 columns p of a row n of a state: chunk i of this thread
+    // A state, 8 columns p of a row n at a time: chunk i of this thread.  Every thread reads its chunks before any writes
+    // its parts over them.
     constexpr int kChunks = P * N / 8 / kGradThreads;
-    auto chunk_off = [&](int i) {
-        const int n = (i * kGradThreads + tid) / (P / 8), p8 = (i * kGradThreads + tid) % (P / 8);
-        return (uint32_t)(p8 >> 3) * L::kSBlock + sw128_offset(n, p8 & 7);
+    auto issue_raw = [&](uint64_t *bar, uint32_t to, const float4 *src, size_t unit, uint32_t from, uint32_t bytes) {
+        mbar_expect_tx(bar, bytes);
+        bulk_load_g2s(sm + to, reinterpret_cast<const uint8_t *>(src + unit * (P * N / 4)) + from, bytes, bar);
     };
+    auto wait_raw = [&] {
+        if (!mbar_wait(bar_r, r_phase)) *abort_flag = 1;
+        r_phase ^= 1;
+    };
+    auto read_raw = [&](int i, bool in_x, float (&x)[8]) {
+        const int n = (i * kGradThreads + tid) % N, p8 = (i * kGradThreads + tid) / N;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t at = (uint32_t)((2 * p8 + u) * N + n) * 16;
+            const float4 v = *reinterpret_cast<const float4 *>(
+                sm + (!in_x ? L::oR + at : at < L::kRawX ? L::oX + at : L::oR + at - L::kRawX));
+            x[4 * u] = v.x;
+            x[4 * u + 1] = v.y;
+            x[4 * u + 2] = v.z;
+            x[4 * u + 3] = v.w;
+        }
+    };
+    auto write_parts = [&](int i, uint32_t third, const float (&x)[8]) {
+        const int n = (i * kGradThreads + tid) % N, p8 = (i * kGradThreads + tid) / N;
+        const uint32_t off = (uint32_t)(p8 >> 3) * L::kSBlock + sw128_offset(n, p8 & 7);
+        float r[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = x[e];
+        *reinterpret_cast<uint4 *>(sm + L::oHi + off) = take_bf16x8(r);
+        *reinterpret_cast<uint4 *>(sm + L::oLo + off) = take_bf16x8(r);
+        *reinterpret_cast<uint4 *>(sm + third + off) = take_bf16x8(r);
+    };
+    // the three parts of a state, the smallest first (the tensor core truncates what it adds to a larger sum)
+    auto part_at = [&](int part, uint32_t third) { return sb + (part == 0 ? third : part == 1 ? L::oLo : L::oHi); };
 #pragma unroll 1
     for (int hh = 0; hh < nh; ++hh) {
         const int h = h0 + hh;
@@ -179,12 +206,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (hh & 1) * SsmGate::kBytes);
         const float *s_dt = s_g + SsmGate::dt;
         if (tid < 2 * P * N * 2 / 128) {  // this head's states on their way into L2: a line of each a thread
-            prefetch_l2(reinterpret_cast<const uint8_t *>(Sin) + unit * 4 * P * N + tid * 128);
-            prefetch_l2(reinterpret_cast<const uint8_t *>(Gout) + unit * 4 * P * N + tid * 128);
+            prefetch_l2(Sin + unit * (P * N / 4) + tid * 8);
+            prefetch_l2(Gout + unit * (P * N / 4) + tid * 8);
         }
         if (tid == 0) {
             if (hh == 0 && !mbar_wait(bar_bc, 0)) *abort_flag = 1;
-            if (!mbar_wait(bar_g, (uint32_t)(hh & 1)) || !mbar_wait(bar_x, (uint32_t)(hh & 1)) ||
+            if (!mbar_wait(bar_g, (uint32_t)(hh & 1)) || !mbar_wait(bar_x, 0) ||
                 !mbar_wait(bar_y, (uint32_t)(hh & 1)))
                 *abort_flag = 1;
         }
@@ -193,13 +220,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         if (*abort_flag) break;
         if (tid == kIo && hh + 1 < nh) issue_g(hh + 1);  // the other table was last read a head ago
         __syncwarp();
-        // ---- W = dY X^T (and once K = C B^T) ----
+        // ---- K = C B^T, W = dY X^T ----
         if (tid == 0) {
             tc_after_sync();
-            if (hh == 0)
 #pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk)
-                    mma_bf16(tmem + tK, desc_k(sb + L::oC, kk), desc_k(sb + L::oB, kk), idesc_bf16(128, 128, false, false), kk > 0);
+            for (int kk = 0; kk < N / 16; ++kk)
+                mma_bf16(tmem + tK, desc_k(sb + L::oC, kk), desc_k(sb + L::oB, kk), idesc_bf16(128, 128, false, false), kk > 0);
 #pragma unroll
             for (int kk = 0; kk < P / 16; ++kk)
                 mma_bf16(tmem + tT, desc_k(sb + L::oY, kk), desc_k(sb + L::oX, kk), idesc_bf16(128, 128, false, false), kk > 0);
@@ -207,11 +233,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         }
         mma_sync_point();
         if (*abort_flag) break;
+        if (tid == kIo) {
+            issue_raw(bar_s, L::oX, Sin, unit, 0, L::kRawX);
+            ++n_s;
+        }
+        __syncwarp();
         // ---- M' = L K, dK = L W Delta, and the sums of R = M' W: rows i, 32 columns j, 16 at a time (with all 32 the
-        // kernel spilled, and beside its shared memory there is next to no L1 for that) ----
+        // kernel spilled, and beside its shared memory there is next to no L1 for that).  The first bf16 parts go to shared
+        // memory, the second wait in TMEM over the K they come from: 8 columns of M', 8 of dK. ----
         {
             uint8_t *dm = sm + L::oM + (prt >> 1) * kTile, *dk = sm + L::oK + (prt >> 1) * kTile;
-            float rsum = 0.f;
+            double rsum = 0.0;
             if (prt > q) {
                 const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -219,7 +251,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                     *reinterpret_cast<uint4 *>(dm + sw128_offset(row, (prt & 1) * 4 + i)) = zero;
                     *reinterpret_cast<uint4 *>(dk + sw128_offset(row, (prt & 1) * 4 + i)) = zero;
                 }
-                s_colp[q * 128 + prt * 32 + lane] = 0.f;
+                s_colp[q * 128 + prt * 32 + lane] = 0.0;
             } else {
                 const float rf = s_g[SsmGate::rowf + row], ci = s_g[SsmGate::hi + row], cl = s_g[SsmGate::lo + row];
                 float dg = 0.f, wd = 0.f;
@@ -231,7 +263,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                     tmem_ld16x2(tl + tK + j0, kv, tl + tT + j0, wv);
                     if (prt < q) {
                         const float2 rf2 = make_float2(rf, rf);
-                        float2 sum2 = make_float2(0.f, 0.f);
                         const float4 *col4 = reinterpret_cast<const float4 *>(s_g + SsmGate::col + (q - 1) * 96 + j0);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -244,7 +275,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                                 const float2 l = fmul2(rf2, c2[u]), w = make_float2(wv[n], wv[n + 1]);
                                 const float2 kk = fmul2(make_float2(kv[n], kv[n + 1]), l), r = fmul2(kk, w);
                                 const float2 dk2 = fmul2(w, fmul2(l, d2[u]));
-                                sum2 = ffma2(r, d2[u], sum2);
                                 kv[n] = kk.x;
                                 kv[n + 1] = kk.y;
                                 rr[n] = r.x;
@@ -253,7 +283,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                                 wv[n + 1] = dk2.y;
                             }
                         }
-                        rsum += sum2.x + sum2.y;
                     } else {
                         const float4 *hi4 = reinterpret_cast<const float4 *>(s_g + SsmGate::hi + j0);
                         const float4 *lo4 = reinterpret_cast<const float4 *>(s_g + SsmGate::lo + j0);
@@ -274,18 +303,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                                 kv[n] = at <= lane ? kv[n] * l[u] : 0.f;
                                 wv[n] = at <= lane ? w * (l[u] * d[u]) : 0.f;
                                 rr[n] = at < lane ? r : 0.f;
-                                rsum = fmaf(rr[n], d[u], rsum);
                             }
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        st_bf16x8(dm + sw128_offset(row, (prt & 1) * 4 + hb * 2 + i), kv + 8 * i);
-                        st_bf16x8(dk + sw128_offset(row, (prt & 1) * 4 + hb * 2 + i), wv + 8 * i);
+                        *reinterpret_cast<uint4 *>(dm + sw128_offset(row, (prt & 1) * 4 + hb * 2 + i)) = take_bf16x8(kv + 8 * i);
+                        *reinterpret_cast<uint4 *>(dk + sw128_offset(row, (prt & 1) * 4 + hb * 2 + i)) = take_bf16x8(wv + 8 * i);
                     }
-                    ssm_column_sums(rr);
-                    if (lane < 16) s_colp[q * 128 + j0 + lane] = rr[0];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        kv[i] = __uint_as_float(take_bf16x2(kv[2 * i], kv[2 * i + 1]));
+                        wv[i] = __uint_as_float(take_bf16x2(wv[2 * i], wv[2 * i + 1]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) kv[8 + i] = wv[i];
+                    tmem_st16(tl + tK + j0, kv);
+                    // 64 bits: a pair's R Delta in its row's sum and in its column's cancels exactly behind both
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        double r[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            r[e] = (double)rr[8 * half + e];
+                            rsum = fma(r[e], (double)s_dt[j0 + 8 * half + e], rsum);
+                        }
+                        ssm_column_sums(r);
+                        if (lane < 8) s_colp[q * 128 + j0 + 8 * half + lane] = r[0];
+                    }
                 }
+                tmem_wait_st();
                 if (prt == q) {
                     s_diag[row] = dg;
                     s_wd[row] = wd;
@@ -296,26 +343,54 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         fence_async_smem();
         tc_before_sync();
         __syncthreads();
-        // ---- the chunk's own products ----
-        if (tid == 0) {
-            tc_after_sync();
+        // ---- the chunk's own products, of the first parts and then of the second ----
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            if (part == 1) {
+                if (prt <= q) {  // above the diagonal the zeros stay
+                    uint8_t *dm = sm + L::oM + (prt >> 1) * kTile, *dk = sm + L::oK + (prt >> 1) * kTile;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_bf16(tmem + tT, desc_mn(sb + L::oM, kk), desc_mn(sb + L::oY, kk), idesc_bf16(128, P, true, true), kk > 0);
+                    for (int hb = 0; hb < 2; ++hb) {
+                        float v[16];
+                        tmem_ld16(tl + tK + prt * 32 + hb * 16, v);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_bf16(tmem + tC, desc_k(sb + L::oK, kk), desc_mn(sb + L::oB, kk), idesc_bf16(128, N, false, true),
-                         hh > 0 || kk > 0);
+                        for (int i = 0; i < 2; ++i) {
+                            *reinterpret_cast<float4 *>(dm + sw128_offset(row, (prt & 1) * 4 + hb * 2 + i)) =
+                                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                            *reinterpret_cast<float4 *>(dk + sw128_offset(row, (prt & 1) * 4 + hb * 2 + i)) =
+                                make_float4(v[8 + 4 * i], v[9 + 4 * i], v[10 + 4 * i], v[11 + 4 * i]);
+                        }
+                    }
+                }
+                fence_async_smem();
+                tc_before_sync();
+                __syncthreads();
+            }
+            if (tid == 0) {
+                tc_after_sync();
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_bf16(tmem + tB, desc_mn(sb + L::oK, kk), desc_mn(sb + L::oC, kk), idesc_bf16(128, N, true, true),
-                         hh > 0 || kk > 0);
-            mma_commit(mma_bar);
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16(tmem + tT, desc_mn(sb + L::oM, kk), desc_mn(sb + L::oY, kk), idesc_bf16(128, P, true, true),
+                             part > 0 || kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16(tmem + tC, desc_k(sb + L::oK, kk), desc_mn(sb + L::oB, kk), idesc_bf16(128, N, false, true),
+                             hh > 0 || part > 0 || kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16(tmem + tB, desc_mn(sb + L::oK, kk), desc_mn(sb + L::oC, kk), idesc_bf16(128, N, true, true),
+                             hh > 0 || part > 0 || kk > 0);
+                mma_commit(mma_bar);
+            }
+            __syncwarp();
+            mma_sync_point();
+            if (*abort_flag) break;
         }
-        __syncwarp();
-        mma_sync_point();
         if (*abort_flag) break;
-        if (tid == kIo) issue_state(&tm_s, unit);  // over M' and dK
+        if (L::kRaw > L::kRawX && tid == kIo) {
+            issue_raw(bar_r, L::oR, Sin, unit, L::kRawX, L::kRaw - L::kRawX);
+            ++n_r;
+        }
         __syncwarp();
         float dxi[PW];  // Delta dXi + D dy
         tmem_ldw<PW>(tl + tT + prt * PW, dxi);
@@ -330,32 +405,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
                 for (int k = 0; k < 8; ++k) dxi[8 * i + k] = a.D ? fmaf(dt, dxi[8 * i + k], D * y[k]) : dt * dxi[8 * i + k];
             }
         }
+        float st[kChunks][8];  // this thread's part of S_in, for <G, S_in>
+        if (!mbar_wait(bar_s, (uint32_t)(hh & 1))) *abort_flag = 1;
+        if (L::kRaw > L::kRawX) wait_raw();
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) read_raw(i, true, st[i]);
+        __syncthreads();
+        if (*abort_flag) break;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) write_parts(i, L::oThirdS, st[i]);
+        fence_async_smem();
         tc_before_sync();
         __syncthreads();
         // ---- T = dY S_in ----
-        wait_state();
         if (tid == 0) {
             tc_after_sync();
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
+            for (int pt = 0; pt < 3; ++pt)
 #pragma unroll
                 for (int kk = 0; kk < P / 16; ++kk)
-                    mma_bf16(tmem + tT, desc_k(sb + L::oY, kk), desc_k(sb + (pt ? L::oLo : L::oHi), kk, L::kSBlock),
+                    mma_bf16(tmem + tT, desc_k(sb + L::oY, kk), desc_k(part_at(pt, L::oThirdS), kk, L::kSBlock),
                              idesc_bf16(128, N, false, false), pt > 0 || kk > 0);
             mma_commit(mma_bar);
         }
         __syncwarp();
-        uint4 sh[kChunks], sl[kChunks];  // this thread's part of S_in, for <G, S_in>
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            sh[i] = *reinterpret_cast<const uint4 *>(sm + L::oHi + chunk_off(i));
-            sl[i] = *reinterpret_cast<const uint4 *>(sm + L::oLo + chunk_off(i));
-        }
         mma_sync_point();
         if (*abort_flag) break;
         if (tid == kIo) {
-            issue_state(&tm_g, unit);
-            if (hh + 1 < nh) issue_y(h + 1);
+            issue_raw(bar_r, L::oR, Gout, unit, 0, L::kRaw);
+            ++n_r;
+            issue_x(h);  // the third part was over it
         }
         __syncwarp();
         {
@@ -379,39 +458,51 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             tmem_wait_st();
             s_syp[prt * 128 + row] = e * dot;
         }
+        wait_raw();
+        {
+            float dot = 0.f;  // <G, S_in>
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                float x[8];
+                read_raw(i, false, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dot = fmaf(x[e], st[i][e], dot);
+                    st[i][e] = x[e];
+                }
+            }
+            __syncthreads();
+            if (*abort_flag) break;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) write_parts(i, L::oThirdG, st[i]);
+            double sum = (double)dot;
+#pragma unroll
+            for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (lane == 0) s_red[warp] = sum;
+        }
+        if (tid == 0 && !mbar_wait(bar_x, 1)) *abort_flag = 1;
+        fence_async_smem();
         tc_before_sync();
         __syncthreads();
+        if (*abort_flag) break;
         // ---- T = X G_out ----
-        wait_state();
         if (tid == 0) {
             tc_after_sync();
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
+            for (int pt = 0; pt < 3; ++pt)
 #pragma unroll
                 for (int kk = 0; kk < P / 16; ++kk)
-                    mma_bf16(tmem + tT, desc_k(sb + L::oX, kk), desc_k(sb + (pt ? L::oLo : L::oHi), kk, L::kSBlock),
+                    mma_bf16(tmem + tT, desc_k(sb + L::oX, kk), desc_k(part_at(pt, L::oThirdG), kk, L::kSBlock),
                              idesc_bf16(128, N, false, false), pt > 0 || kk > 0);
             mma_commit(mma_bar);
         }
         __syncwarp();
-        {
-            float dot = 0.f;  // <G, S_in>, each from its two parts
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                float x[8], y[8], v[8], w[8];
-                ld8s(sm + L::oHi + chunk_off(i), x);
-                ld8s(sm + L::oLo + chunk_off(i), y);
-                ld8s(reinterpret_cast<const uint8_t *>(&sh[i]), v);
-                ld8s(reinterpret_cast<const uint8_t *>(&sl[i]), w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) dot = fmaf(x[e] + y[e], v[e] + w[e], dot);
-            }
-            dot = warp_sum(dot, 32);
-            if (lane == 0) s_red[warp] = dot;
-        }
         mma_sync_point();
         if (*abort_flag) break;
-        if (tid == kIo && hh + 1 < nh) issue_x(h + 1);
+        if (tid == kIo && hh + 1 < nh) {
+            issue_x(h + 1);
+            issue_y(h + 1);
+        }
         __syncwarp();
         {
             const float el = s_g[SsmGate::el + row], w = el * s_dt[row];
@@ -440,19 +531,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
         if (tid == 0) {
             tc_after_sync();
 #pragma unroll
-            for (int kk = 0; kk < N / 16; ++kk)
-                mma_bf16(tmem + tT, desc_k(sb + L::oB, kk), desc_mn(sb + L::oHi, kk, L::kSBlock), idesc_bf16(128, P, false, true),
-                         kk > 0);
+            for (int pt = 1; pt < 3; ++pt)
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk)
+                    mma_bf16(tmem + tT, desc_k(sb + L::oB, kk), desc_mn(part_at(pt, 0), kk, L::kSBlock),
+                             idesc_bf16(128, P, false, true), pt > 1 || kk > 0);
             mma_commit(mma_bar);
         }
         __syncwarp();
         if (warp >= 4 && warp < 8) {
             const int t = tid - 128, w4 = warp - 4;
-            const float cg = (s_colp[t] + s_colp[128 + t] + s_colp[256 + t] + s_colp[384 + t]) +
-                             (s_gxp[t] + s_gxp[128 + t] + s_gxp[256 + t] + s_gxp[384 + t]);
-            const float rw = s_rowp[t] + s_rowp[128 + t] + s_rowp[256 + t] + s_rowp[384 + t], dt = s_dt[t];
+            const double cg = (s_colp[t] + s_colp[128 + t] + s_colp[256 + t] + s_colp[384 + t]) +
+                              (double)(s_gxp[t] + s_gxp[128 + t] + s_gxp[256 + t] + s_gxp[384 + t]);
+            const double rw = s_rowp[t] + s_rowp[128 + t] + s_rowp[256 + t] + s_rowp[384 + t], dt = (double)s_dt[t];
             const double suf = (double)(s_syp[t] + s_syp[128 + t] + s_syp[256 + t] + s_syp[384 + t]);
-            const double pre = (double)fmaf(dt, cg, -rw);  // the difference of the sums is what cancels: 64 bits from here
+            const double pre = fma(dt, cg, -rw);
             const double pre_in = ssm_warp_scan(pre), suf_in = ssm_warp_scan(suf);
             if (lane == 31) {
                 s_tw[w4] = pre_in;
@@ -460,25 +553,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
             double before = pre_in - pre, after = suf - suf_in;
-            float cross = lane < 16 ? s_red[lane] : 0.f;
+            double cross = 0.0;
+#pragma unroll
+            for (int w = 0; w < 16; ++w) cross += s_red[w];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 if (w < w4) before += s_tw[w];
                 if (w >= w4) after += s_tw[4 + w];
             }
-            cross = warp_sum(cross, 32) * s_g[SsmGate::elast];
-            const float dlog = (float)(before + after + (double)cross);
-            float raw = fmaf(s_g[SsmGate::A], dlog, cg + s_diag[t]) * s_g[SsmGate::sig + t], sA = 0.f, sD = 0.f;
+            const double dlog = before + after + cross * (double)s_g[SsmGate::elast];
+            double raw = ((double)s_g[SsmGate::A] * dlog + cg + (double)s_diag[t]) * (double)s_g[SsmGate::sig + t], sA = 0.0, sD = 0.0;
             if (t < valid) {
-                a.ddelta[((size_t)b * a.T + t0 + t) * a.H + h] = raw;
+                a.ddelta[((size_t)b * a.T + t0 + t) * a.H + h] = (float)raw;
                 sA = dt * dlog;
-                sD = s_wd[t];
+                sD = (double)s_wd[t];
             } else {
-                raw = 0.f;
+                raw = 0.0;
             }
-            sA = warp_sum(sA, 32);
-            raw = warp_sum(raw, 32);
-            sD = warp_sum(sD, 32);
+#pragma unroll
+            for (int off = 16; off; off >>= 1) {
+                sA += __shfl_xor_sync(0xffffffffu, sA, off);
+                raw += __shfl_xor_sync(0xffffffffu, raw, off);
+                sD += __shfl_xor_sync(0xffffffffu, sD, off);
+            }
             if (lane == 0) {
                 s_tot[w4 * 3] = sA;
                 s_tot[w4 * 3 + 1] = raw;
@@ -507,7 +604,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             bulk_commit();
         }
         __syncwarp();
-        if (tid < 3) part[tid * units + unit] = (double)(s_tot[tid] + s_tot[3 + tid] + s_tot[6 + tid] + s_tot[9 + tid]);
+        if (tid < 3) part[tid * units + unit] = s_tot[tid] + s_tot[3 + tid] + s_tot[6 + tid] + s_tot[9 + tid];
     }
     if (*abort_flag) {
         if (tid == 0 && mma_open) mbar_wait(mma_bar, mma_phase ^ 1);
@@ -518,6 +615,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
             mbar_wait(bar_y, (uint32_t)((n_y - 1) & 1));
             mbar_wait(bar_g, (uint32_t)((n_g - 1) & 1));
             if (n_s > 0) mbar_wait(bar_s, (uint32_t)((n_s - 1) & 1));
+            if (n_r > 0) mbar_wait(bar_r, (uint32_t)((n_r - 1) & 1));
             bulk_wait_all();
         }
     } else {
@@ -621,38 +719,36 @@ cudaError_t ssm_tc_bwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     const int nch = (a.T + kTcQ - 1) / kTcQ;
     const SsmTcBwdWs w = ssm_tc_bwd_ws(a.B, a.T, a.H, a.G, P, N);
     uint8_t *base = static_cast<uint8_t *>(ws);
-    __nv_bfloat16 *st = reinterpret_cast<__nv_bfloat16 *>(base + w.st), *g = reinterpret_cast<__nv_bfloat16 *>(base + w.g);
+    float4 *st = reinterpret_cast<float4 *>(base + w.st), *g = reinterpret_cast<float4 *>(base + w.g);
     float *segS = reinterpret_cast<float *>(base + w.segS), *segG = reinterpret_cast<float *>(base + w.segG);
     float *dec = reinterpret_cast<float *>(base + w.dec);
     double *part = reinterpret_cast<double *>(base + w.part);
     float *dBp = reinterpret_cast<float *>(base + w.dBp), *dCp = reinterpret_cast<float *>(base + w.dCp);
-    const size_t units = (size_t)a.B * nch * a.H;
     float *gates = reinterpret_cast<float *>(base + w.gates);
-    CUtensorMap mx, mb, mc, my, mdx, ms, mg;
+    CUtensorMap mx, mb, mc, my, mdx;
     if (!ssm_token_map(&mx, a.x, a.B, a.T, a.H, P, a.ldx) || !ssm_token_map(&mb, a.Bm, a.B, a.T, a.G, N, a.ldb) ||
         !ssm_token_map(&mc, a.Cm, a.B, a.T, a.G, N, a.ldc) || !ssm_token_map(&my, a.dy, a.B, a.T, a.H, P, a.H * P) ||
-        !ssm_token_map(&mdx, a.dx, a.B, a.T, a.H, P, a.H * P) ||
-        !ssm_state_map(&ms, st, units, P, N) || !ssm_state_map(&mg, g, units, P, N))
+        !ssm_token_map(&mdx, a.dx, a.B, a.T, a.H, P, a.H * P))
         return cudaErrorInvalidValue;
     cudaError_t e = ssm_launch_gates(a, gates, s);
     const dim3 grid(2u * (unsigned)(a.B * a.H) * (unsigned)w.R);
     const size_t smem = SsmWalkTc<P, N>::kAlloc;
     if (e == cudaSuccess && w.R > 1) {
-        e = ssm_launch(ssm_tc_walk_kernel<P, N, false>, grid, SsmWalkTc<P, N>::kThreads, smem, s, mx, mb, my, mc, ms, mg, a, w.m, 2,
-                       (const float *)gates, segS, segG, dec);
+        e = ssm_launch(ssm_tc_walk_kernel<P, N, false>, grid, SsmWalkTc<P, N>::kThreads, smem, s, mx, mb, my, mc, a, w.m, 2,
+                       (const float *)gates, st, g, segS, segG, dec);
         if (e == cudaSuccess && w.R > kJoinMost) {
             e = ssm_launch_scan(false, a.B, w.R, a.H, P * N, segS, dec, a.S0, nullptr, s);
             if (e == cudaSuccess) e = ssm_launch_scan(true, a.B, w.R, a.H, P * N, segG, dec, a.dS_T, nullptr, s);
         }
     }
     if (e == cudaSuccess)
-        e = ssm_launch(ssm_tc_walk_kernel<P, N, true>, grid, SsmWalkTc<P, N>::kThreads, smem, s, mx, mb, my, mc, ms, mg, a, w.m, 2,
-                       (const float *)gates, segS, segG, dec);
+        e = ssm_launch(ssm_tc_walk_kernel<P, N, true>, grid, SsmWalkTc<P, N>::kThreads, smem, s, mx, mb, my, mc, a, w.m, 2,
+                       (const float *)gates, st, g, segS, segG, dec);
     const int per = (a.H / a.G + w.splits - 1) / w.splits;
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_grad_kernel<P, N>, dim3((unsigned)((size_t)a.B * nch * a.G * w.splits)), kGradThreads,
-                       (size_t)SsmGradTc<P, N>::kAlloc, s, mx, mb, mc, my, mdx, ms, mg, a, w.splits, per,
-                       (const float *)gates, (const __nv_bfloat16 *)st, (const __nv_bfloat16 *)g, dBp, dCp, part);
+                       (size_t)SsmGradTc<P, N>::kAlloc, s, mx, mb, mc, my, mdx, a, w.splits, per,
+                       (const float *)gates, (const float4 *)st, (const float4 *)g, dBp, dCp, part);
     if (e != cudaSuccess) return e;
     if (w.splits > 1) {
         const long long total4 = (long long)a.B * a.T * a.G * (N / 4);

@@ -80,15 +80,6 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t base, int kk, uint32_t bloc
 __device__ __forceinline__ void ld8s(const uint8_t *p, float *v) {
     load8(reinterpret_cast<const __nv_bfloat16 *>(p), v);
 }
-// v as two bf16 parts: v = hi + lo up to 2^-17 |v|.
-__device__ __forceinline__ void st_split8(uint8_t *hi, uint8_t *lo, float *v) {
-    float r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
-    sm100::st_bf16x8(hi, v);
-    sm100::st_bf16x8(lo, r);
-}
-
 // ---- 0. gates ---------------------------------------------------------------------------
 // One table per unit = (b, chunk, head), read by the other kernels as one bulk copy: computed in place by a warp of
 // each of them, the softplus and the 64-bit sums took 4600 of a chunk's 9100 cycles.  Floats at:
@@ -147,18 +138,6 @@ __global__ void __launch_bounds__(128) ssm_gate_kernel(SsmArgs a, float *__restr
 }
 
 // ---- 1. walks over the chunks ------------------------------------------------------------
-// A state's two bf16 parts in memory: [unit][part][N][P], unit = (b, chunk, head).
-inline bool ssm_state_map(CUtensorMap *map, const void *base, size_t units, int P, int N) {
-    SsmEncodeFn enc = ssm_encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)P, (cuuint64_t)N, 2, (cuuint64_t)units};
-    const cuuint64_t strides[3] = {(cuuint64_t)P * 2, (cuuint64_t)N * P * 2, (cuuint64_t)2 * N * P * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)N, 1, 1}, estr[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Up to this many segments are joined by every reader itself (it reads the sums of the segments before its own);
 // ssm_scan_kernel joins more.  B=4 T=4096 H=16 P=N=128, 2 segments: 136 us, with the scan's launch 144 us.
 constexpr int kJoinMost = 8;
@@ -192,10 +171,10 @@ __device__ __forceinline__ void ssm_enter_segment(float (&v)[W], const float *se
 
 // A CTA walks the chunks of one (b, h, segment), forwards (S <- e^{c_last} S + B^T (w X)) or, rev, backwards (G <-
 // e^{c_last} G + C^T (e^c dY)), the state in registers and a chunk's own sum in TMEM (lanes n, columns p, fp32), the
-// weighted rows in three bf16 parts (OUT: two).
-// OUT: from the state that enters the segment, every chunk's entering state is written as two bf16 parts (out_S, out_G
-// through tm_s, tm_g), and dS0 at the end.  Otherwise: from zero, the segment's own sum goes to seg_S or seg_G
-// [b][seg][h][P][N] in fp32, and its decay to dec.
+// weighted rows in three bf16 parts.
+// OUT: from the state that enters the segment, every chunk's entering state is written to out_S or out_G (fp32,
+// [unit][P / 4][N][4], unit = (b, chunk, head): a warp writes 512 bytes at once), and dS0 at the end.  Otherwise: from
+// zero, the segment's own sum goes to seg_S or seg_G [b][seg][h][P][N], and its decay to dec.
 // Two or three stages of operands: while a chunk's products run, the next chunk's rows are weighted (without states to
 // write a chunk takes about 3900 cycles at P = N = 128; with one stage and half the warps it took 4500, and 9400 with
 // states stored row by row against 5600 now).  What bounds it is the operands' way from L2: 64 KB a chunk and SM.
@@ -205,20 +184,17 @@ struct SsmWalkTc {
     static constexpr int ST = P == 64 ? 3 : 2;                           // stages
     static constexpr uint32_t XB = P / 64 * kTile, BB = N / 64 * kTile, kStage = 2 * XB + BB;
     static constexpr uint32_t oX = 0, oLo = XB, oB = 2 * XB, oZero = ST * kStage;  // X, weighted in place; its second part
-    static constexpr uint32_t kSBlock = N * 128, SB = P / 64 * kSBlock;  // a state part as a tile: N rows
-    static constexpr uint32_t oOut = oZero + (N == 64 ? kTile : 0);      // OUT: a state's second part on its way out
-    static constexpr uint32_t oThird = oOut;                             // otherwise: the weighted rows' third part
+    static constexpr uint32_t oThird = oZero + (N == 64 ? kTile : 0);    // the third part: of one chunk at a time
     static constexpr uint32_t kGate = 128 * 4 + 64;                      // the rows' weights and the decay
-    static constexpr uint32_t oGate = oOut + (SB > XB ? SB : XB), oCtl = oGate + 2 * kGate;
+    static constexpr uint32_t oGate = oThird + XB, oCtl = oGate + 2 * kGate;
     static constexpr uint32_t kAlloc = oCtl + 96 + 1024;
 };
 
 template <int P, int N, bool OUT>
 __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
-    const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_c,
-    const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_g, SsmArgs a, int m, int dirs,
-    const float *__restrict__ gates, float *__restrict__ seg_S, float *__restrict__ seg_G, float *__restrict__ dec) {
+    const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_c, SsmArgs a, int m, int dirs,
+    const float *__restrict__ gates, float4 *__restrict__ out_S, float4 *__restrict__ out_G, float *__restrict__ seg_S, float *__restrict__ seg_G, float *__restrict__ dec) {
     using L = SsmWalkTc<P, N>;
     using namespace sm100;
     constexpr int PW = L::PW;
@@ -307,7 +283,7 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             for (int e = 0; e < 8; ++e) x[e] *= w;
             *reinterpret_cast<uint4 *>(p) = take_bf16x8(x);
             second[i] = take_bf16x8(x);
-            if (!OUT) third[i] = take_bf16x8(x);
+            third[i] = take_bf16x8(x);
         }
     };
     auto convert_third = [&] {  // the products of the chunk before are done
@@ -347,9 +323,6 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
 #pragma unroll 1
     for (; k < cn && !*abort_flag; ++k) {
         const float *s_g = reinterpret_cast<const float *>(sm + L::oGate + (k & 1) * L::kGate) + 128 - SsmGate::misc;
-        // A state leaves through the second-part buffer of the stage of the chunk before (its products are done) and a
-        // buffer of its own.
-        uint8_t *out_hi = sm + ((k + ST - 1) % ST) * L::kStage + L::oLo, *out_lo = sm + L::oOut;
         const float el = s_g[SsmGate::elast];
         const bool update = keep || k + 1 < cn;
         edge += *reinterpret_cast<const double *>(s_g + SsmGate::last);
@@ -359,40 +332,32 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             if (ST == 2) prefetch(k + 3);
         }
         __syncwarp();
-        if (!OUT) convert_third();
-        if (OUT && row < N)
+        convert_third();
+        if (OUT && row < N) {
+            float4 *dst = (rev ? out_G : out_S) + ((((size_t)b * nch + chunk(k)) * a.H + h) * (P / 4) + cp / 4) * N + row;
 #pragma unroll
-            for (int i = 0; i < PW / 8; ++i) {
-                const uint32_t off = (uint32_t)(cp >> 6) * L::kSBlock + sw128_offset(row, ((cp & 63) >> 3) + i);
-                st_split8(out_hi + off, out_lo + off, v + 8 * i);
-            }
+            for (int i = 0; i < PW / 4; ++i) dst[(size_t)i * N] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
         fence_async_smem();
         tc_before_sync();
         __syncthreads();
-        const int unit = (int)(((size_t)b * nch + chunk(k)) * a.H + h);
-        if (OUT && tid == kIo) {
-            for (int pt = 0; pt < 2; ++pt)
-                for (int i = 0; i < P / 64; ++i)
-                    tma_store_4d(rev ? &tm_g : &tm_s, (pt ? out_lo : out_hi) + i * L::kSBlock, i * 64, 0, pt, unit);
-            bulk_commit();
-        }
         if (tid == 0 && update) {
             tc_after_sync();
             const uint32_t st = sb + (k % ST) * L::kStage, at = st + L::oB;
             const uint32_t block = N == 64 ? sb + L::oZero - at : kTile;  // the second 64 lanes
 #pragma unroll
-            for (int part = OUT ? 1 : 2; part >= 0; --part)
+            for (int part = 2; part >= 0; --part)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     mma_bf16(tmem, desc_mn(at, kk, block), desc_mn(part == 2 ? sb + L::oThird : st + (part ? L::oLo : L::oX), kk),
-                             idesc_bf16(128, P, true, true), part < (OUT ? 1 : 2) || kk > 0);
+                             idesc_bf16(128, P, true, true), part < 2 || kk > 0);
             mma_commit(mma_bar);
         }
         __syncwarp();
-        if (k + 1 < cn) convert(k + 1);
-        if (OUT && tid == kIo) bulk_wait_read_all();
-        if (OUT && ST == 2) __syncthreads();  // out_hi is where the next second part goes
-        if (k + 1 < cn) convert_second(k + 1);
+        if (k + 1 < cn) {
+            convert(k + 1);
+            convert_second(k + 1);
+        }
         fence_async_smem();
         if (tid == 0 && update) {
             mma_open = !mbar_wait(mma_bar, (uint32_t)(k & 1));
@@ -418,7 +383,6 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             record_status(GDR_ERR_TIMEOUT);
             for (int i = n_t > ST ? n_t - ST : 0; i < n_t; ++i) mbar_wait(tma_bar + i % ST, (uint32_t)(i / ST) & 1);
             for (int i = n_g > 1 ? n_g - 2 : 0; i < n_g; ++i) mbar_wait(bar_g + (i & 1), (uint32_t)(i >> 1) & 1);
-            if (OUT) bulk_wait_all();
         }
         if (tid == 0 && mma_open) mbar_wait(mma_bar, (uint32_t)((k - 1) & 1));
     } else {
@@ -428,7 +392,6 @@ __global__ void __launch_bounds__(512, 1) ssm_tc_walk_kernel(
             for (int i = 0; i < PW; ++i) dst[(size_t)(cp + i) * N + row] = v[i];
         }
         if (!OUT && !rev && tid == 0) dec[((size_t)b * R + seg) * a.H + h] = exp2f((float)edge);
-        if (OUT && tid == kIo) bulk_wait_all();
     }
     tc_before_sync();
     __syncthreads();
@@ -881,7 +844,7 @@ cudaError_t ssm_tc_fwd(const SsmArgs &a, void *ws, cudaStream_t s) {
     float *st = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.st);
     float *dec = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.dec);
     e = ssm_launch(ssm_tc_walk_kernel<P, N, false>, grid, SsmWalkTc<P, N>::kThreads, (size_t)SsmWalkTc<P, N>::kAlloc, s, mx, mb,
-                   mx, mb, mx, mx, a, m, 1, (const float *)gates, st, (float *)nullptr, dec);
+                   mx, mb, a, m, 1, (const float *)gates, (float4 *)nullptr, (float4 *)nullptr, st, (float *)nullptr, dec);
     if (e == cudaSuccess && R > kJoinMost) e = ssm_launch_scan(false, a.B, R, a.H, P * N, st, dec, a.S0, a.S_T, s);
     if (e == cudaSuccess)
         e = ssm_launch(ssm_tc_y_kernel<P, N, false>, grid, SsmYTc<P, N, false>::NT, (size_t)SsmYTc<P, N, false>::kAlloc, s, mx,

@@ -425,8 +425,10 @@ GDR_API gdr_status gdr_seg_fixup(int B, int T, int H, int dk, int dv, gdr_dtype 
  *   Supported: P, N in {64, 128}; H a multiple of G; B*T*H*max(P,N) < 2^31;
  *   B, H <= 65535.  workspace: gdr_ssm_fwd_workspace_bytes(...)
  *   bytes; NULL or short -> GDR_ERR_WORKSPACE.  Repeated calls give the same bits.
- *   bf16: products take bf16 operands, but what leaves in fp32 does so to about
- *   2^-18 of the terms that it sums (states, weighted rows as two bf16 parts).
+ *   bf16 inputs: everything between them and the outputs is held to fp32's
+ *   accuracy (operands of the tensor cores that are not bf16 themselves are
+ *   split into bf16 parts): fp32 outputs are as exact as fp32 operations, bf16
+ *   outputs one rounding away from that.
  *   An output at the address of an input (S_T = S0, y = x) is refused, here and
  *   in the scan's and the convolution's other calls.
  */

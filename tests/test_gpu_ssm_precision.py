@@ -50,7 +50,23 @@ def test_forward(size, s0):
     within(y, r["y"].cpu(), (BF * r["y"].abs() + (2 * 2.0 ** -17 + sums(d)) * m["y"]).cpu(), "y")
 
 
-@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("s0", [True, False])
+@pytest.mark.parametrize("size", SIZES)
+def test_gradients(size, s0):
+    d = lasting(size, sum(size) + 1, s0)
+    g = bwd(d, want_dS0=s0)
+    r, m, p = scan_blocks(d, grads=True), scan_blocks(d, grads=True, absolute=True), scan_blocks(d, grads=True, dtype=torch.float32)
+    for n in ("ddelta", "dS0"):  # (the others of fp32 are sums of few values whose terms cancel: elementwise alone)
+        if g[n] is not None:
+            as_exact_as_fp32(g[n], r[n], p[n], n)
+    for n in ("ddelta", "dA", "dD", "ddelta_bias", "dS0"):
+        if g[n] is not None:
+            within(g[n], r[n].cpu(), 2 * sums(d) * m[n].cpu(), n)
+    for n in ("dx", "dB", "dC"):
+        within(g[n], r[n].cpu(), (BF * r[n].abs() + (3 * 2.0 ** -17 + 2 * sums(d)) * m[n]).cpu(), n)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("size", [(3, 414, 16, 2, 64, 64), (3, 206, 16, 1, 128, 128), (2, 333, 8, 2, 128, 64), (1, 1500, 16, 1, 64, 128)])
 def test_sums_over_tokens(size, dtype):
     """dA and the bias's gradient: every pair of tokens enters them once through a row's sum and once, with the other sign,

@@ -57,7 +57,7 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
 // Wait until the phase with parity `parity` has completed; false on timeout.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns = kWaitNs) {
     const uint32_t addr = smem_u32(bar);
-    uint64_t t0 = 0;  // read at the 256th poll: a wait that ends soon does not pay for the timer
+    const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 1;; ++it) {
         uint32_t done;
         asm volatile(
@@ -68,11 +68,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
             : "r"(addr), "r"(parity)
             : "memory");
         if (done) return true;
-        if ((it & 255u) == 0) {
-            const uint64_t now = global_timer_ns();
-            if (t0 == 0) t0 = now;
-            else if (now - t0 > limit_ns) return false;
-        }
+        if ((it & 255u) == 0 && global_timer_ns() - t0 > limit_ns) return false;
     }
 }
 
@@ -80,7 +76,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
 // CTA of the cluster: a remote arrive or a DSMEM bulk copy).
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
     const uint32_t addr = smem_u32(bar);
-    uint64_t t0 = 0;  // read at the 256th poll: a wait that ends soon does not pay for the timer
+    const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 1;; ++it) {
         uint32_t done;
         asm volatile(
@@ -91,11 +87,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
             : "r"(addr), "r"(parity)
             : "memory");
         if (done) return true;
-        if ((it & 255u) == 0) {
-            const uint64_t now = global_timer_ns();
-            if (t0 == 0) t0 = now;
-            else if (now - t0 > kWaitNs) return false;
-        }
+        if ((it & 255u) == 0 && global_timer_ns() - t0 > kWaitNs) return false;
     }
 }
 

@@ -12,7 +12,7 @@
 // two windows, the taps and their sums take 165 registers: held to 128 it spilled
 // and lost 4 us, held to 96 it took 151 us).
 #pragma once
-#include "common.cuh"
+#include "launch.cuh"
 
 namespace gdr {
 
@@ -533,8 +533,8 @@ cudaError_t conv_fwd_launch(ConvArgs a, cudaStream_t s) {
     a.run = conv_fwd_run(a.B, a.T, a.C, V, 148 * (K <= 4 && sizeof(T) == 2 ? 3 : 2), sizeof(T) == 2 ? 64 : 32);
     a.runs = (a.T + a.run - 1) / a.run;
     const long long warps = (long long)((a.C + 32 * V - 1) / (32 * V)) * a.runs * a.B;
-    const size_t smem = V == 4 ? (size_t)8 * ConvRing<T, V, kConvFwdU, kConvFwdGroups>::kBytes : 0;
-    cudaError_t e = cudaFuncSetAttribute(conv_fwd_kernel<T, V, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t smem = V == 4 ? (size_t)8 * ConvRing<T, V, kConvFwdU, kConvFwdGroups>::kBytes : 0;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(conv_fwd_kernel<T, V, K>), smem);
     if (e != cudaSuccess) return e;
     conv_fwd_kernel<T, V, K><<<(unsigned)((warps + 7) / 8), 256, smem, s>>>(a);
     g_launches.fetch_add(1, std::memory_order_relaxed);
@@ -546,9 +546,9 @@ cudaError_t conv_bwd_launch(ConvArgs a, float *dw, float *dbias, cudaStream_t s)
     const int slots = plan.slots;
     a.run = plan.run;
     a.runs = (a.T + a.run - 1) / a.run;
-    const size_t rings = V == 4 ? (size_t)2 * kConvBwdWarps * ConvRing<T, V, kConvBwdU, kConvBwdGroups>::kBytes : 0, red = (size_t)kConvBwdWarps * (K + 1) * 32 * V * 4;
-    const size_t smem = rings > red ? rings : red;
-    cudaError_t e = cudaFuncSetAttribute(conv_bwd_kernel<T, V, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t rings = V == 4 ? (size_t)2 * kConvBwdWarps * ConvRing<T, V, kConvBwdU, kConvBwdGroups>::kBytes : 0;
+    constexpr size_t red = (size_t)kConvBwdWarps * (K + 1) * 32 * V * 4, smem = rings > red ? rings : red;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(conv_bwd_kernel<T, V, K>), smem);
     if (e != cudaSuccess) return e;
     conv_bwd_kernel<T, V, K><<<dim3((a.C + 32 * V - 1) / (32 * V), slots), kConvBwdWarps * 32, smem, s>>>(a, slots);
     conv_sum_kernel<<<dim3((a.C + 31) / 32, K + 1), 256, 0, s>>>(slots, K, a.C, a.part, dw, dbias);

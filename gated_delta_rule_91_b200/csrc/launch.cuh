@@ -1,0 +1,41 @@
+// launch.cuh -- the host side of a launch: a kernel's shared memory limit and
+// the blocks of it that fit an SM, asked of the driver once per device.
+#pragma once
+#include <mutex>
+
+#include "common.cuh"
+
+namespace gdr {
+
+// Every kernel is launched with one dynamic shared memory size and block size of its own, so that no call lowers a limit that
+// another thread is about to launch under.  Past the table's end the driver is asked every time (a microsecond of the
+// host's time).
+inline cudaError_t prepare_kernel(const void *kernel, size_t smem, int threads = 0, int *blocks = nullptr) {
+    constexpr int kMost = 1024;
+    struct Entry {
+        const void *kernel;
+        int device, blocks;
+    };
+    static std::mutex mu;
+    static Entry table[kMost];
+    static int count = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < count; ++i)
+        if (table[i].kernel == kernel && table[i].device == dev) {
+            if (blocks) *blocks = table[i].blocks;
+            return cudaSuccess;
+        }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    int fit = 0, sms = 0;
+    if (e == cudaSuccess && blocks) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem);
+    if (e == cudaSuccess && blocks) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (blocks) *blocks = fit * sms;
+    if (count < kMost) table[count++] = Entry{kernel, dev, fit * sms};
+    return cudaSuccess;
+}
+
+}  // namespace gdr

@@ -456,17 +456,13 @@ struct NormBwd {
     static cudaError_t go(NormArgs a, float *dw, float *db, cudaStream_t s) {
         constexpr int per = NT / TPR;
         auto kernel = norm_bwd_kernel<T, V, TPR, NV, NT>;
-        const size_t sums = NT > TPR ? (size_t)(NT / TPR) * 2 * a.D * 4 : 0, ring = NormRing<V, NV, NT>::kBytes;
-        const size_t smem = sums > ring ? sums : ring;
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the instance's largest D: a limit that followed this call's D could be lowered under another thread's launch
+        constexpr size_t sums = NT > TPR ? (size_t)per * 2 * (TPR * NV * V) * 4 : 0, ring = NormRing<V, NV, NT>::kBytes;
+        constexpr size_t smem = sums > ring ? sums : ring;
+        int most = 0;  // one wave: a second one of a few blocks would cost as much as the first
+        cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), smem, NT, &most);
         if (e != cudaSuccess) return e;
-        // one wave: a second one of a few blocks would cost as much as the first
-        int fit = 1, sms = 148, dev = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, NT, smem);
-        if (e == cudaSuccess) e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        long long grid = (a.R + per - 1) / per, most = (long long)sms * fit;
+        long long grid = (a.R + per - 1) / per;
         if (most > kNormBwdMaxBlocks) most = kNormBwdMaxBlocks;
         if (grid > most) grid = most;
         kernel<<<(unsigned)grid, NT, smem, s>>>(a);

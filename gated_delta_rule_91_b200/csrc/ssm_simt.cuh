@@ -12,8 +12,7 @@
 // summed index outermost.  fp32 B=3 T=777 H=6 P=N=64: 42 us; gradients of B=2 T=333
 // H=4 P=128 N=64: 76 us (latency: 48 to 234 blocks of one to three a SM).
 #pragma once
-#include <mutex>
-
+#include "launch.cuh"
 #include "ssm_common.cuh"
 
 namespace gdr {
@@ -586,30 +585,9 @@ inline cudaError_t ssm_launch_scan(bool rev, int B, int nch, int H, int PN, floa
     return cudaGetLastError();
 }
 
-// Raises a kernel's shared memory limit once per device (a microsecond of the host's time each); past the table's end,
-// every time.
-inline cudaError_t ssm_allow_smem(const void *kernel, size_t smem) {
-    constexpr int kMost = 256;
-    static std::mutex mu;
-    static const void *kernels[kMost];
-    static int devices[kMost], count = 0;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < count; ++i)
-        if (kernels[i] == kernel && devices[i] == dev) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && count < kMost) {
-        kernels[count] = kernel;
-        devices[count++] = dev;
-    }
-    return e;
-}
-// Every kernel is launched with one shared memory size of its own.
 template <typename K, typename... A>
 cudaError_t ssm_launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-    cudaError_t e = ssm_allow_smem(reinterpret_cast<const void *>(kernel), smem);
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     kernel<<<grid, threads, smem, s>>>(args...);
     g_launches.fetch_add(1, std::memory_order_relaxed);

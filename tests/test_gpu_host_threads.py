@@ -1,0 +1,56 @@
+"""Calls from several host threads at once, each on its own stream."""
+import threading
+
+import pytest
+import torch
+
+import gated_delta_rule_91_b200 as gdr
+
+pytestmark = pytest.mark.gpu
+
+
+def together(*work):
+    """Runs the callables in threads of their own; raises what any of them raised."""
+    wrong, start = [], threading.Barrier(len(work))
+
+    def run(f):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                f()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=run, args=(f,)) for f in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if wrong:
+        raise wrong[0]
+
+
+def test_layer_norm_gradients_of_two_widths():
+    """Widths that share a kernel and differ in the shared memory that they need of it."""
+    def work(D):
+        g = torch.Generator().manual_seed(D)
+        h, dy = (torch.randn(64, D, generator=g).cuda() for _ in range(2))
+        w = torch.ones(D, device="cuda")
+        want = [u.clone() for u in gdr.gdr_layernorm_bwd(h, w, dy)]
+        torch.cuda.synchronize()
+
+        dx, dw, db = (torch.empty_like(u) for u in (h, w, w))
+        L = gdr.lib()
+        ws = torch.empty(L.gdr_layernorm_bwd_workspace_bytes(D), dtype=torch.uint8, device="cuda")
+
+        def run():
+            args = (64, D, gdr.GDR_F32, h.data_ptr(), w.data_ptr(), 1e-5, dy.data_ptr(), None, dx.data_ptr(), dw.data_ptr(),
+                    db.data_ptr(), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+            for _ in range(10000):  # the entry itself: little of a call is outside it
+                gdr.check(L.gdr_layernorm_bwd(*args))
+            torch.cuda.current_stream().synchronize()
+            assert all(torch.equal(a, b) for a, b in zip((dx, dw, db), want))
+        return run
+
+    together(work(33), work(127), work(3))

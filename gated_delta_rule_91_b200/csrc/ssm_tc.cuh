@@ -43,13 +43,15 @@ typedef CUresult (*SsmEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, 
                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 inline SsmEncodeFn ssm_encode_fn() {
-    static SsmEncodeFn fn = nullptr;
+    static std::atomic<SsmEncodeFn> known{nullptr};  // several threads may ask first
+    SsmEncodeFn fn = known.load(std::memory_order_relaxed);
     if (!fn) {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<SsmEncodeFn>(p);
+        known.store(fn, std::memory_order_relaxed);
     }
     return fn;
 }
@@ -769,14 +771,13 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
 
 // ---- host side ------------------------------------------------------------------------------
 inline int ssm_sm_count() {
-    static int n = 0;
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed);
     if (n == 0) {
-        int dev = 0, v = 0;
-        if (cudaGetDevice(&dev) == cudaSuccess &&
-            cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-            n = v;
-        else
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return 148;
+        known.store(n, std::memory_order_relaxed);
     }
     return n;
 }

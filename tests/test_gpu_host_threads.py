@@ -54,3 +54,21 @@ def test_layer_norm_gradients_of_two_widths():
         return run
 
     together(work(33), work(127), work(3))
+
+
+def test_scans_of_several_sizes():
+    from test_gpu_ssm import bwd, fwd, inputs
+
+    def work(size):
+        d = inputs(*size, "bf16", seed=sum(size))
+        want = fwd(d) + tuple(bwd(d).values())
+        torch.cuda.synchronize()
+
+        def run():
+            for _ in range(20):
+                got = fwd(d) + tuple(bwd(d).values())
+            torch.cuda.current_stream().synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        return run
+
+    together(work((1, 700, 2, 1, 64, 128)), work((2, 300, 4, 2, 128, 128)), work((1, 130, 3, 1, 64, 64)))

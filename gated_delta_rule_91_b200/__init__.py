@@ -394,15 +394,20 @@ def _mismatch(name, t, shape, dtype, device):
     raise ValueError("%s must be on the CUDA device of the other tensors (%s), got %s" % (name, device, t.device))
 
 
-def _like(name, t, shape, dtype, device):
-    """`t` (None passes) as a dense operand of this shape, type and (CUDA) device; returns its address."""
+def _like(name, t, shape, dtype, device, keep=None):
+    """`t` (None passes) as a dense operand of this shape, type and (CUDA) device; returns its address.  The library takes
+    operands that start on 16 bytes: an input (`keep`: a list that outlives the launch) that does not is copied."""
     if t is None:
         return None
     if t.shape != shape or t.dtype is not dtype or t.device != device:
         _mismatch(name, t, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    at = t.data_ptr()
+    if at & 15 and keep is not None:
+        keep.append(t.clone())
+        at = keep[-1].data_ptr()
+    return at
 
 
 def _ints(*sizes):
@@ -411,13 +416,14 @@ def _ints(*sizes):
         raise ValueError("sizes and strides must be below 2^31, got %s" % (sizes,))
 
 
-def _rows(name, t, shape, lead, dtype, device):
+def _rows(name, t, shape, lead, dtype, device, keep):
     """`t` as rows of a wider buffer: the axes from `lead` on are a dense row, and the rows of the leading axes are
-    one stride apart.  Returns (address, stride in elements; 0: dense)."""
+    one stride apart.  Returns (address, stride in elements; 0: dense), of a dense copy in `keep` where `t` does not start
+    on 16 bytes."""
     if t.shape != shape or t.dtype is not dtype or t.device != device:
         _mismatch(name, t, shape, dtype, device)
     if t.is_contiguous():
-        return t.data_ptr(), 0
+        return _like(name, t, shape, dtype, device, keep), 0
     strides = t.stride()
     width = 1
     for i in range(len(shape) - 1, lead - 1, -1):
@@ -435,6 +441,9 @@ def _rows(name, t, shape, lead, dtype, device):
                 raise ValueError("%s: the rows of all batches must be one stride apart" % name)
             rows *= shape[i]
     _ints(ld)
+    if t.data_ptr() & 15:
+        keep.append(t.contiguous())
+        return keep[-1].data_ptr(), 0
     return t.data_ptr(), ld
 
 
@@ -462,7 +471,7 @@ def _scratch(nbytes, device, workspace):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, lead):
+def _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, lead, keep):
     """Sizes, type and addresses of the scan's inputs; lead = 2: [B,T,...], 1: [B,...]."""
     dev, dt = _cuda(x, "x"), _dt(x)
     if x.dim() != lead + 2 or Bm.dim() != lead + 2:
@@ -470,14 +479,14 @@ def _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, lead):
     H, P = x.shape[-2:]
     G, N = Bm.shape[-2:]
     rows = x.shape[:lead]
-    px, ldx = _rows("x", x, x.shape, lead, x.dtype, dev)
-    pb, ldb = _rows("Bm", Bm, rows + (G, N), lead, x.dtype, dev)
-    pc, ldc = _rows("Cm", Cm, rows + (G, N), lead, x.dtype, dev)
+    px, ldx = _rows("x", x, x.shape, lead, x.dtype, dev, keep)
+    pb, ldb = _rows("Bm", Bm, rows + (G, N), lead, x.dtype, dev, keep)
+    pc, ldc = _rows("Cm", Cm, rows + (G, N), lead, x.dtype, dev, keep)
     f = torch.float32
-    pd = _like("delta", delta, rows + (H,), f, dev)
-    pA = _like("A", A, (H,), f, dev)
-    pD = _like("D", D, (H,), f, dev)
-    pbias = _like("delta_bias", delta_bias, (H,), f, dev)
+    pd = _like("delta", delta, rows + (H,), f, dev, keep)
+    pA = _like("A", A, (H,), f, dev, keep)
+    pD = _like("D", D, (H,), f, dev, keep)
+    pbias = _like("delta_bias", delta_bias, (H,), f, dev, keep)
     return rows, H, G, P, N, dt, dev, (px, ldx, pd, pA, pb, ldb, pc, ldc, pD, pbias)
 
 
@@ -487,14 +496,15 @@ def gdr_ssm_fwd(x, delta, A, Bm, Cm, D=None, delta_bias=None, S0=None, *, softpl
     Delta = softplus(delta + delta_bias) or delta + delta_bias.  x [B,T,H,P]; Bm, Cm [B,T,G,N] (H/G heads share a
     group); all three may be slices of one [B,T,channels] buffer.  delta [B,T,H], A, D, delta_bias [H] fp32; S0
     [B,H,P,N] fp32.  Returns (y, S_T or None)."""
-    (B, T), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 2)
+    keep = []
+    (B, T), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 2, keep)
     y = x.new_empty((B, T, H, P)) if y is None else y
     if S_T is None and return_state:
         S_T = delta.new_empty((B, H, P, N))
     f = torch.float32
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_ssm_fwd_workspace_bytes(B, T, H, G, P, N, dt), dev, workspace)
-    _launch(dev, L.gdr_ssm_fwd, B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev),
+    _launch(dev, L.gdr_ssm_fwd, B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev, keep),
             _like("y", y, (B, T, H, P), x.dtype, dev), _like("S_T", S_T, (B, H, P, N), f, dev),
             ws.data_ptr(), ws_bytes)
     return y, S_T
@@ -504,7 +514,8 @@ def gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, dy, dS_T=None, *, softpl
                 workspace=None):
     """Backward of gdr_ssm_fwd.  Returns dict(dx, ddelta, dA, dB, dC, dD, ddelta_bias, dS0); dD and ddelta_bias are
     None without D and delta_bias."""
-    (B, T), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 2)
+    keep = []
+    (B, T), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 2, keep)
     f = torch.float32
     like = torch.empty_like  # the dense ones
     out = dict(dx=x.new_empty((B, T, H, P)), ddelta=like(delta), dA=like(A), dB=x.new_empty((B, T, G, N)),
@@ -513,8 +524,8 @@ def gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, dy, dS_T=None, *, softpl
                dS0=delta.new_empty((B, H, P, N)) if want_dS0 else None)
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_ssm_bwd_workspace_bytes(B, T, H, G, P, N, dt), dev, workspace)
-    _launch(dev, L.gdr_ssm_bwd, B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev),
-            _like("dy", dy, (B, T, H, P), x.dtype, dev), _like("dS_T", dS_T, (B, H, P, N), f, dev),
+    _launch(dev, L.gdr_ssm_bwd, B, T, H, G, P, N, dt, int(softplus), *ptrs, _like("S0", S0, (B, H, P, N), f, dev, keep),
+            _like("dy", dy, (B, T, H, P), x.dtype, dev, keep), _like("dS_T", dS_T, (B, H, P, N), f, dev, keep),
             *(None if t is None else t.data_ptr() for t in out.values()), ws.data_ptr(), ws_bytes)
     return out
 
@@ -522,7 +533,8 @@ def gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, dy, dS_T=None, *, softpl
 def gdr_ssm_step(x, delta, A, Bm, Cm, S, D=None, delta_bias=None, *, softplus=False, y=None):
     """One token of gdr_ssm_fwd: x [B,H,P]; Bm, Cm [B,G,N]; delta [B,H]; S [B,H,P,N] fp32 advanced in place.
     Returns y [B,H,P]."""
-    (B,), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 1)
+    keep = []
+    (B,), H, G, P, N, dt, dev, ptrs = _ssm_operands(x, delta, A, Bm, Cm, D, delta_bias, 1, keep)
     y = x.new_empty((B, H, P)) if y is None else y
     if S is None:
         raise ValueError("S is required")
@@ -532,24 +544,25 @@ def gdr_ssm_step(x, delta, A, Bm, Cm, S, D=None, delta_bias=None, *, softplus=Fa
     return y
 
 
-def _conv_operands(x, w, bias, conv_state):
+def _conv_operands(x, w, bias, conv_state, keep):
     dev, dt = _cuda(x, "x"), _dt(x)
     if x.dim() != 3 or w.dim() != 2:
         raise ValueError("x must be [B,T,C] and w [C,K], got %s and %s" % (tuple(x.shape), tuple(w.shape)))
     B, T, C = x.shape
     K = w.shape[1]
     _ints(B, T, C, K)
-    px, ldx = _rows("x", x, x.shape, 2, x.dtype, dev)
-    return (B, T, C, K, dt, dev, (px, ldx, _like("w", w, (C, K), torch.float32, dev),
-                                  _like("bias", bias, (C,), torch.float32, dev),
-                                  _like("conv_state", conv_state, (B, max(K - 1, 0), C), x.dtype, dev)))
+    px, ldx = _rows("x", x, x.shape, 2, x.dtype, dev, keep)
+    return (B, T, C, K, dt, dev, (px, ldx, _like("w", w, (C, K), torch.float32, dev, keep),
+                                  _like("bias", bias, (C,), torch.float32, dev, keep),
+                                  _like("conv_state", conv_state, (B, max(K - 1, 0), C), x.dtype, dev, keep)))
 
 
 def gdr_conv_fwd(x, w, bias=None, *, conv_state=None, conv_state_out=None, silu=True, y=None):
     """Depthwise causal convolution of width K with SiLU: x [B,T,C] (rows of a wider buffer are read in place), w
     [C,K] and bias [C] fp32.  conv_state [B,K-1,C] (dtype of x) carries the inputs before token 0; conv_state_out
     receives the last K-1 inputs and may be conv_state itself.  A decode token is T = 1.  Returns y [B,T,C]."""
-    B, T, C, K, dt, dev, ptrs = _conv_operands(x, w, bias, conv_state)
+    keep = []
+    B, T, C, K, dt, dev, ptrs = _conv_operands(x, w, bias, conv_state, keep)
     y = x.new_empty((B, T, C)) if y is None else y
     _launch(dev, lib().gdr_conv_fwd, B, T, C, K, dt, int(silu), *ptrs,
             _like("conv_state_out", conv_state_out, (B, max(K - 1, 0), C), x.dtype, dev),
@@ -561,7 +574,8 @@ def gdr_conv_bwd(x, w, dy, bias=None, *, conv_state=None, dconv_state_out=None, 
                  want_dconv_state=None, workspace=None):
     """Backward of gdr_conv_fwd.  Returns dict(dx, dw, dbias (None unless a bias was given or want_dbias),
     dconv_state (None unless conv_state was given or want_dconv_state))."""
-    B, T, C, K, dt, dev, ptrs = _conv_operands(x, w, bias, conv_state)
+    keep = []
+    B, T, C, K, dt, dev, ptrs = _conv_operands(x, w, bias, conv_state, keep)
     f = torch.float32
     want_db = (bias is not None) if want_dbias is None else want_dbias
     want_ds = (conv_state is not None) if want_dconv_state is None else want_dconv_state
@@ -570,8 +584,8 @@ def gdr_conv_bwd(x, w, dy, bias=None, *, conv_state=None, dconv_state_out=None, 
                dconv_state=torch.empty(B, max(K - 1, 0), C, dtype=x.dtype, device=dev) if want_ds else None)
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_conv_bwd_workspace_bytes(B, T, C, K), dev, workspace)
-    _launch(dev, L.gdr_conv_bwd, B, T, C, K, dt, int(silu), *ptrs, _like("dy", dy, (B, T, C), x.dtype, dev),
-            _like("dconv_state_out", dconv_state_out, (B, max(K - 1, 0), C), x.dtype, dev),
+    _launch(dev, L.gdr_conv_bwd, B, T, C, K, dt, int(silu), *ptrs, _like("dy", dy, (B, T, C), x.dtype, dev, keep),
+            _like("dconv_state_out", dconv_state_out, (B, max(K - 1, 0), C), x.dtype, dev, keep),
             *(None if t is None else t.data_ptr() for t in out.values()), ws.data_ptr(), ws_bytes)
     return out
 
@@ -584,10 +598,10 @@ def gdr_layernorm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, 
     y = x.new_empty(x.shape) if y is None else y
     if residual is not None and h is None:
         h = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    f = torch.float32
-    _launch(dev, lib().gdr_layernorm_fwd, x.numel() // max(D, 1), D, dt, _like("x", x, x.shape, x.dtype, dev),
-            _like("residual", residual, x.shape, x.dtype, dev),
-            _like("weight", weight, (D,), f, dev), _like("bias", bias, (D,), f, dev),
+    f, keep = torch.float32, []
+    _launch(dev, lib().gdr_layernorm_fwd, x.numel() // max(D, 1), D, dt, _like("x", x, x.shape, x.dtype, dev, keep),
+            _like("residual", residual, x.shape, x.dtype, dev, keep),
+            _like("weight", weight, (D,), f, dev, keep), _like("bias", bias, (D,), f, dev, keep),
             float(eps), _like("y", y, x.shape, x.dtype, dev),
             _like("h", h, x.shape, x.dtype, dev))
     return y, h
@@ -598,15 +612,15 @@ def gdr_layernorm_bwd(h, weight, dy, *, dres=None, eps=1e-5, want_dbias=True, wo
     reaches h along the residual stream.  Returns (dx, dweight, dbias or None)."""
     dev, dt, D = _cuda(h, "h"), _dt(h), h.shape[-1]
     _ints(D)
-    f = torch.float32
+    f, keep = torch.float32, []
     dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
     dweight = torch.empty(D, dtype=f, device=dev)
     dbias = torch.empty(D, dtype=f, device=dev) if want_dbias else None
     L = lib()
     ws, ws_bytes = _scratch(L.gdr_layernorm_bwd_workspace_bytes(D), dev, workspace)
-    _launch(dev, L.gdr_layernorm_bwd, h.numel() // max(D, 1), D, dt, _like("h", h, h.shape, h.dtype, dev),
-            _like("weight", weight, (D,), f, dev), float(eps),
-            _like("dy", dy, h.shape, h.dtype, dev), _like("dres", dres, h.shape, h.dtype, dev),
+    _launch(dev, L.gdr_layernorm_bwd, h.numel() // max(D, 1), D, dt, _like("h", h, h.shape, h.dtype, dev, keep),
+            _like("weight", weight, (D,), f, dev, keep), float(eps),
+            _like("dy", dy, h.shape, h.dtype, dev, keep), _like("dres", dres, h.shape, h.dtype, dev, keep),
             dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
             ws.data_ptr(), ws_bytes)
     return dx, dweight, dbias

@@ -127,7 +127,7 @@ def block_prologue(xq, xk, xv, wq, wk, wv, bq=None, bk=None, bv=None, conv_state
 def _dense_rows(x, lead):
     """x itself where the library reads it in place (rows of a wider buffer), a dense copy otherwise."""
     if x.is_contiguous():
-        return x
+        return x if x.data_ptr() % 16 == 0 else x.clone()
     shape, strides, width = x.shape, x.stride(), 1
     for i in range(len(shape) - 1, lead - 1, -1):
         if shape[i] > 1 and strides[i] != width:

@@ -498,15 +498,26 @@ __global__ void __launch_bounds__(256) conv_sum_kernel(int slots, int K, int C, 
 }
 
 // ---- host side ------------------------------------------------------------------------------
-// Tokens per run of the forward: the shortest of 8, 16, .. 88 whose blocks are on the SMs all at once (blocks: how many
-// of the launch fit); a larger problem takes 64 of bf16, 32 of fp32.  A longer run reads fewer taps and windows, a
-// shorter one keeps more SMs at work.  C=2304 K=4: B=4 T=4096 bf16 36 us (88; 32: 39, 16: 43) and fp32 59 (32; 88: 66),
-// T=65536 bf16 111 us (64; 32: 119), T=512 10 us (16; 64: 16).
-inline int conv_fwd_run(int B, int T, int C, int V, int blocks, int otherwise) {
+// Tokens per run of the forward: of 8, 16, .. 160 the one whose rounds of blocks (`fit` of them at once) come to the
+// fewest tokens, 8 more a run for its taps and window.  fp32 up to K = 4 is nearer to HBM and takes at most 40.  C=2304, us
+// of the chosen run (others): bf16 K=4 B=4 T=512 8.6 (16; 64: 12.7), T=4096 34.9 (88; 16: 39.2, 64: 34.7, 104: 39.0), T=4400
+// 37.0 (96; 64: 39.2, 128: 44.7), T=6000 45.4 (128; 32: 49.5, 160: 53.6), T=65536 at B=1 107 (112; 32: 117, 160: 115); K=7
+// T=4400 49.5 (144; 32: 78, 64: 64); fp32 K=4 T=4096 54.7 (32; 16: 57.7, 64: 58.5, 128: 62).  Over 36 such sizes the choice
+// costs 1 % more than the best of all.
+inline int conv_fwd_run(int B, int T, int C, int K, int V, bool f32, int fit) {
     const long long cols = (C + 32 * V - 1) / (32 * V);
-    for (int run = 8; run <= 88; run += 8)
-        if ((cols * ((T + run - 1) / run) * B + 7) / 8 <= blocks) return run;
-    return otherwise;
+    const int most = f32 && K <= 4 ? 40 : 160;
+    long long best = -1;
+    int at = 8;
+    for (int run = 8; run <= most; run += 8) {
+        const long long blocks = (cols * ((T + run - 1) / run) * B + 7) / 8;
+        const long long cost = (blocks + fit - 1) / fit * ((run < T ? run : T) + 8);
+        if (best < 0 || cost < best) {
+            best = cost;
+            at = run;
+        }
+    }
+    return at;
 }
 // The backward is one launch that fits (slots x columns, three blocks an SM up to K = 4); a warp's runs are as long as
 // their number stays the same for every warp and no run passes 192 tokens.  C=2304 K=4 bf16: B=4 T=4096 61 us (172;
@@ -515,7 +526,7 @@ struct ConvPlan {
     int run, slots;
 };
 inline ConvPlan conv_bwd_plan(int B, int T, int C, int K, int V) {
-    const long long cols = (C + 32 * V - 1) / (32 * V), fit = 148 * (K <= 4 ? 3 : 2) / cols, room = fit < 1 ? 1 : fit;
+    const long long cols = (C + 32 * V - 1) / (32 * V), fit = sm_count() * (K <= 4 ? 3 : 2) / cols, room = fit < 1 ? 1 : fit;
     const long long warps = room * kConvBwdWarps, need = (T + 191) / 192;
     const long long trips = (B * need + warps - 1) / warps;
     const long long runs = warps * trips / B;  // per sequence, at least `need`
@@ -529,13 +540,13 @@ inline ConvPlan conv_bwd_plan(int B, int T, int C, int K, int V) {
 
 template <typename T, int V, int K>
 cudaError_t conv_fwd_launch(ConvArgs a, cudaStream_t s) {
-    // three blocks an SM of bf16 up to K = 4 (their bound on registers), two otherwise (the ring of fp32)
-    a.run = conv_fwd_run(a.B, a.T, a.C, V, 148 * (K <= 4 && sizeof(T) == 2 ? 3 : 2), sizeof(T) == 2 ? 64 : 32);
+    constexpr size_t smem = V == 4 ? (size_t)8 * ConvRing<T, V, kConvFwdU, kConvFwdGroups>::kBytes : 0;
+    int fit = 0;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(conv_fwd_kernel<T, V, K>), smem, 256, &fit);
+    if (e != cudaSuccess) return e;
+    a.run = conv_fwd_run(a.B, a.T, a.C, K, V, sizeof(T) == 4, fit > 0 ? fit : 1);
     a.runs = (a.T + a.run - 1) / a.run;
     const long long warps = (long long)((a.C + 32 * V - 1) / (32 * V)) * a.runs * a.B;
-    constexpr size_t smem = V == 4 ? (size_t)8 * ConvRing<T, V, kConvFwdU, kConvFwdGroups>::kBytes : 0;
-    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(conv_fwd_kernel<T, V, K>), smem);
-    if (e != cudaSuccess) return e;
     conv_fwd_kernel<T, V, K><<<(unsigned)((warps + 7) / 8), 256, smem, s>>>(a);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cudaGetLastError();

@@ -38,4 +38,17 @@ inline cudaError_t prepare_kernel(const void *kernel, size_t smem, int threads =
     return cudaSuccess;
 }
 
+// SMs of the device of the first call (148 where there is none: workspace sizes are asked for on hosts too).
+inline int sm_count() {
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return 148;
+        known.store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 }  // namespace gdr

@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
 // and with several of them partial sums in fp32 and a launch that adds them.  Measured: B=4 T=4096 H=16, one CTA 309 us
 // (two: 335); B=1 T=4096, four 148 us (eight: 162, two: 186); B=2 T=1024 H=4 G=2, one 69 us (two: 72).
 inline int ssm_grad_splits(int B, int T, int H, int G) {
-    const int nch = (T + kTcQ - 1) / kTcQ, HG = H / G, sms = ssm_sm_count();
+    const int nch = (T + kTcQ - 1) / kTcQ, HG = H / G, sms = sm_count();
     int best = 1;
     double cost = -1;
     for (int s = 1; s <= HG; ++s) {
@@ -673,7 +673,7 @@ inline int ssm_grad_splits(int B, int T, int H, int G) {
 // T=4096 H=16 P=N=128, uncut 308 us (2 segments: 415); B=1 T=4096, 4 segments 146 us (8: 157); B=1 T=2048 H=8 P=64, uncut
 // 73 us (4 segments: 82).
 inline int ssm_walk_chunks(int B, int T, int H) {
-    const int nch = (T + kTcQ - 1) / kTcQ, sms = ssm_sm_count();
+    const int nch = (T + kTcQ - 1) / kTcQ, sms = sm_count();
     double best = 1e30;
     int at = nch;
     for (int m = nch; m >= 1; m = m > 64 ? m * 3 / 4 : m - 1) {

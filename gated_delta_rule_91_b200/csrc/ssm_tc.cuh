@@ -770,24 +770,12 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
 }
 
 // ---- host side ------------------------------------------------------------------------------
-inline int ssm_sm_count() {
-    static std::atomic<int> known{0};
-    int n = known.load(std::memory_order_relaxed);
-    if (n == 0) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return 148;
-        known.store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
 // Chunks per segment.  In units of a chunk of the output kernel: whole rounds of CTAs over the SMs, where two CTAs of P =
 // 64 on an SM take 1.75 of one's time; a cut costs the walk over the segments first (about half of that) and two
 // launches.  Measured: B=4 T=4096 H=16 P=N=128, 2 segments 145 us (3: over 164); B=1 T=4096, 8 segments 51 us (16: 56);
 // B=8 T=2048 H=16 P=64, uncut 90 us (2 segments: 102); B=1 T=65536 P=64, 37 segments 307 us (32: 330).
 inline int ssm_tc_chunks(int B, int T, int H, int P) {
-    const int nch = (T + kTcQ - 1) / kTcQ, sms = ssm_sm_count();
+    const int nch = (T + kTcQ - 1) / kTcQ, sms = sm_count();
     double best = 1e30;
     int at = nch;
     for (int m = nch; m >= 1; m = m > 64 ? m * 3 / 4 : m - 1) {

@@ -33,6 +33,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "sm100.cuh"
 
 namespace gdr {
@@ -520,9 +521,9 @@ inline bool make_token_map(CUtensorMap *map, const void *base, int B, int T, int
     const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2, (cuuint64_t)T * H * d * 2};
     const cuuint32_t box[4] = {64, 1, (cuuint32_t)kChunk, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
+    return encode_map(enc, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 inline cudaError_t launch_fwd_tc(int B, int T, int H, const void *q, const void *k, const void *v,

@@ -1,5 +1,6 @@
 // launch.cuh -- the host side of a launch: a kernel's shared memory limit and
-// the blocks of it that fit an SM, asked of the driver once per device.
+// the blocks of it that fit an SM, asked of the driver once per device, the
+// number of SMs, and tensor maps.
 #pragma once
 #include <mutex>
 
@@ -49,6 +50,15 @@ inline int sm_count() {
         known.store(n, std::memory_order_relaxed);
     }
     return n;
+}
+
+// A tensor map by the driver's encoder, which needs the device's context current in this thread.  The runtime makes it so at
+// a thread's first call that needs it, which may be behind this one (an autograd thread, for instance).
+template <typename F, typename... A>
+bool encode_map(F encode, A... a) {
+    if (encode(a...) == 0) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode(a...) == 0;
 }
 
 }  // namespace gdr

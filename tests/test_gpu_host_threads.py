@@ -72,3 +72,38 @@ def test_scans_of_several_sizes():
         return run
 
     together(work((1, 700, 2, 1, 64, 128)), work((2, 300, 4, 2, 128, 128)), work((1, 130, 3, 1, 64, 64)))
+
+
+@pytest.mark.parametrize("name", ["gdr_ssm_fwd", "gdr_ssm_bwd", "gdr_fwd", "gdr2_fwd"])
+def test_the_first_cuda_call_of_a_thread(name):
+    """A thread that has called nothing of CUDA yet, as an autograd thread may be: buffers are all there."""
+    import synth
+    from test_gpu_ssm import inputs
+
+    d = inputs(1, 140, 2, 1, 64, 64, "bf16", seed=4)
+    x = {k: v.cuda() if torch.is_tensor(v) else v
+         for k, v in (synth.gdr2_inputs if name == "gdr2_fwd" else synth.gdr_inputs)(1, 70, 2, 128, 128, "bf16", seed=5).items()}
+    ins = (d["x"], d["delta"], d["A"], d["Bm"], d["Cm"], d["D"], d["bias"], d["S0"])
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    o, S = torch.empty_like(x["v"]), torch.empty(1, 2, 128, 128, device="cuda")
+    y, S_T = torch.empty(1, 140, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.empty_like(d["S0"])
+    call = {"gdr_ssm_fwd": lambda: gdr.gdr_ssm_fwd(*ins, softplus=True, y=y, S_T=S_T, workspace=ws),
+            "gdr_ssm_bwd": lambda: tuple(gdr.gdr_ssm_bwd(*ins, d["dy"], softplus=True, workspace=ws).values()),
+            "gdr_fwd": lambda: gdr.gdr_fwd(*(x[k] for k in ("q", "k", "v", "log_alpha", "beta")), o=o, S_T=S, workspace=ws),
+            "gdr2_fwd": lambda: gdr.gdr2_fwd(*(x[k] for k in ("q", "k", "v", "log_alpha", "b", "w")), o=o, S_T=S, workspace=ws)}[name]
+    want = [u.clone() for u in call()]
+    torch.cuda.synchronize()
+    got, wrong = [], []
+
+    def run():
+        try:
+            got.extend(call())
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    thread = threading.Thread(target=run)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert not wrong, wrong[0]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -6,7 +6,7 @@ S0=None)` does the same for Gated DeltaNet-2 through gdr2_bwd.  The forward
 and the backward are the library's CUDA calls: these classes only save the
 inputs and hand the incoming gradients over (the backward recomputes the
 forward's states itself, so nothing else is kept).  Unused outputs arrive as
-zero gradients.  `block_prologue(...)` (ShortConv, SiLU, q/k L2) and
+zero gradients (to the scan, the convolution and the layer norm as none).  `block_prologue(...)` (ShortConv, SiLU, q/k L2) and
 `block_epilogue(o, g, weight, eps)` (RMSNorm, weight, SiLU gate) are the
 block's steps around the recurrence, differentiated through
 gdr_block_prologue_bwd and gdr_block_epilogue_bwd.  `selective_scan(x, delta, A,
@@ -152,6 +152,7 @@ class SelectiveScan(torch.autograd.Function):
         x, Bm, Cm = (_dense_rows(t, 2) for t in (x, Bm, Cm))
         delta, S0 = _c(delta), _c(S0)
         ctx.softplus = softplus
+        ctx.set_materialize_grads(False)
         ctx.save_for_backward(x, delta, A, Bm, Cm, D, delta_bias, S0)
         return gdr_ssm_fwd(x, delta, A, Bm, Cm, D, delta_bias, S0, softplus=softplus)
 
@@ -159,8 +160,9 @@ class SelectiveScan(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, dS_T):
         x, delta, A, Bm, Cm, D, delta_bias, S0 = ctx.saved_tensors
-        g = gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, _c(dy), _c(dS_T), softplus=ctx.softplus,
-                        want_dS0=S0 is not None)
+        dy = torch.zeros_like(x, memory_format=torch.contiguous_format) if dy is None else _c(dy)
+        g = gdr_ssm_bwd(x, delta, A, Bm, Cm, D, delta_bias, S0, dy, _c(dS_T), softplus=ctx.softplus,
+                        want_dS0=S0 is not None and ctx.needs_input_grad[7])
         return g["dx"], g["ddelta"], g["dA"], g["dB"], g["dC"], g["dD"], g["ddelta_bias"], g["dS0"], None
 
 
@@ -183,7 +185,8 @@ class ShortConv(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, w, bias, conv_state = ctx.saved_tensors
-        g = gdr_conv_bwd(x, w, _c(dy), bias, conv_state=conv_state, silu=ctx.silu)
+        g = gdr_conv_bwd(x, w, _c(dy), bias, conv_state=conv_state, silu=ctx.silu, want_dbias=ctx.needs_input_grad[2],
+                         want_dconv_state=ctx.needs_input_grad[3])
         return g["dx"], g["dw"], g["dbias"], g["dconv_state"], None
 
 
@@ -199,7 +202,8 @@ class LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, residual, eps):
         x, residual = _c(x), _c(residual)
         y, h = gdr_layernorm_fwd(x, weight, bias, residual=residual, eps=eps)
-        ctx.eps, ctx.has_bias, ctx.has_residual = eps, bias is not None, residual is not None
+        ctx.eps, ctx.has_residual = eps, residual is not None
+        ctx.set_materialize_grads(False)
         ctx.save_for_backward(x if h is None else h, weight)
         return y, h
 
@@ -207,8 +211,8 @@ class LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, dh):
         h, weight = ctx.saved_tensors
-        dx, dweight, dbias = gdr_layernorm_bwd(h, weight, _c(dy), dres=_c(dh) if ctx.has_residual else None, eps=ctx.eps,
-                                               want_dbias=ctx.has_bias)
+        dy = torch.zeros_like(h) if dy is None else _c(dy)
+        dx, dweight, dbias = gdr_layernorm_bwd(h, weight, dy, dres=_c(dh), eps=ctx.eps, want_dbias=ctx.needs_input_grad[2])
         return dx, dweight, dbias, dx if ctx.has_residual else None, None
 
 

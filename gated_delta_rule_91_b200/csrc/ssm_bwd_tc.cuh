@@ -649,9 +649,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
 }
 
 // ---- host side ------------------------------------------------------------------------------
-// CTAs per group of heads: a CTA costs about half a head's time beside its heads (C B^T, the first loads, dB and dC),
-// and with several of them partial sums in fp32 and a launch that adds them.  Measured: B=4 T=4096 H=16, one CTA 309 us
-// (two: 335); B=1 T=4096, four 148 us (eight: 162, two: 186); B=2 T=1024 H=4 G=2, one 69 us (two: 72).
+// CTAs per group of heads: a CTA costs about half a head's time beside its heads (the first loads, dB and dC), and with
+// several of them partial sums in fp32 and a launch that adds them.  Measured: B=4 T=4096 H=16 P=N=128, one CTA 441 us (two:
+// 466); B=1 T=4096, four 174 us (eight: 188, two: 241); B=2 T=1024 H=4 G=2 P=64, two 62 us (one: 70).
 inline int ssm_grad_splits(int B, int T, int H, int G) {
     const int nch = (T + kTcQ - 1) / kTcQ, HG = H / G, sms = sm_count();
     int best = 1;
@@ -659,7 +659,7 @@ inline int ssm_grad_splits(int B, int T, int H, int G) {
     for (int s = 1; s <= HG; ++s) {
         const int per = (HG + s - 1) / s;
         if ((HG + per - 1) / per != s) continue;
-        const double c = (double)(((long long)B * nch * G * s + sms - 1) / sms) * (per + (s > 1 ? 1.0 : 0.5)) + (s > 1 ? 1.0 : 0.0);
+        const double c = (double)(((long long)B * nch * G * s + sms - 1) / sms) * (per + (s > 1 ? 0.7 : 0.5)) + (s > 1 ? 0.3 : 0.0);
         if (cost < 0 || c < cost) {
             cost = c;
             best = s;
@@ -669,9 +669,9 @@ inline int ssm_grad_splits(int B, int T, int H, int G) {
 }
 
 // Chunks per segment of the walk: rounds of chunks over the SMs (one CTA each, both directions); a cut costs the
-// segments' own sums first (a chunk there about 0.8 of one with its states written) and three launches.  Measured: B=4
-// T=4096 H=16 P=N=128, uncut 308 us (2 segments: 415); B=1 T=4096, 4 segments 146 us (8: 157); B=1 T=2048 H=8 P=64, uncut
-// 73 us (4 segments: 82).
+// segments' own sums first (a chunk there about 0.8 of one with its states written) and one to three launches.  Measured:
+// B=4 T=4096 H=16 P=N=128, uncut 441 us (2 segments: 545); B=1 T=4096, 4 segments 173 us (1: 231, 8: 189); B=1 T=2048 H=8 P=64,
+// 8 segments 66 us (1: 85, 4: 72, 16: 78).
 inline int ssm_walk_chunks(int B, int T, int H) {
     const int nch = (T + kTcQ - 1) / kTcQ, sms = sm_count();
     double best = 1e30;
@@ -679,7 +679,7 @@ inline int ssm_walk_chunks(int B, int T, int H) {
     for (int m = nch; m >= 1; m = m > 64 ? m * 3 / 4 : m - 1) {
         const int R = (nch + m - 1) / m;
         const double rounds = (double)((2LL * B * H * R + sms - 1) / sms);
-        const double cost = R == 1 ? rounds * (m + 2.0) : rounds * (1.8 * m + 4.0) + 12.0;
+        const double cost = R == 1 ? rounds * (m + 2.0) : rounds * (1.8 * m + 4.0) + (R > kJoinMost ? 4.0 : 1.0);
         if (cost < best * 0.999) {
             best = cost;
             at = m;

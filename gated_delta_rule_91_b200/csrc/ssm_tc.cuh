@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(128) ssm_gate_kernel(SsmArgs a, float *__restr
 
 // ---- 1. walks over the chunks ------------------------------------------------------------
 // Up to this many segments are joined by every reader itself (it reads the sums of the segments before its own);
-// ssm_scan_kernel joins more.  B=4 T=4096 H=16 P=N=128, 2 segments: 136 us, with the scan's launch 144 us.
+// ssm_scan_kernel joins more.  B=4 T=4096 H=16 P=N=128, 2 segments: 175 us, with the scan's launch 183 us; B=1, 8
+// segments: 58 us and 60 us.
 constexpr int kJoinMost = 8;
 
 // The state entering segment seg (leaving it, rev), columns cp .. cp + W - 1 of row n: from the scanned segments, or
@@ -771,9 +772,10 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
 
 // ---- host side ------------------------------------------------------------------------------
 // Chunks per segment.  In units of a chunk of the output kernel: whole rounds of CTAs over the SMs, where two CTAs of P =
-// 64 on an SM take 1.75 of one's time; a cut costs the walk over the segments first (about half of that) and two
-// launches.  Measured: B=4 T=4096 H=16 P=N=128, 2 segments 145 us (3: over 164); B=1 T=4096, 8 segments 51 us (16: 56);
-// B=8 T=2048 H=16 P=64, uncut 90 us (2 segments: 102); B=1 T=65536 P=64, 37 segments 307 us (32: 330).
+// 64 on an SM take 1.5 of one's time; a cut costs the walk over the segments first (about half of that) and two
+// launches.  Measured: B=4 T=4096 H=16 P=N=128, 2 segments 175 us (1: 249, 3: 228); B=1 T=4096, 8 segments 58 us (6: 73, 16:
+// 65); B=8 T=2048 H=16 P=64, uncut 107 us (2 segments: 117); B=1 T=65536 P=64, 37 segments 376 us (16: 404, 32: 411); B=2
+// T=2048 H=24 P=64, 6 segments 55 us (3: 64, 8: 69).
 inline int ssm_tc_chunks(int B, int T, int H, int P) {
     const int nch = (T + kTcQ - 1) / kTcQ, sms = sm_count();
     double best = 1e30;
@@ -781,7 +783,7 @@ inline int ssm_tc_chunks(int B, int T, int H, int P) {
     for (int m = nch; m >= 1; m = m > 64 ? m * 3 / 4 : m - 1) {
         const int R = (nch + m - 1) / m;
         const long long n = (long long)B * H * R, rounds = (n + sms - 1) / sms;
-        const double y = P == 64 && R > 1 && n > sms ? (double)((n + 2 * sms - 1) / (2 * sms)) * 1.75 : (double)rounds;
+        const double y = P == 64 && R > 1 && n > sms ? (double)((n + 2 * sms - 1) / (2 * sms)) * 1.5 : (double)rounds;
         const double cost = R == 1 ? y * 1.1 * m : y * m + (double)rounds * (0.5 * m + 1.0) + 2.0;
         if (cost < best * 0.999) {
             best = cost;

@@ -107,7 +107,10 @@ __global__ void __launch_bounds__(128) ssm_gate_kernel(SsmArgs a, float *__restr
         if (a.bias) z += a.bias[h];
         d = a.softplus ? ssm_softplus(z) : z;
     }
+    // 2^-1e6 is 0 and 2^1e6 infinite in any case; without the bound a sum past the float range has no first part (a NaN stays)
     double c_in = (double)a.A[h] * (double)d * 1.4426950408889634074;
+    if (c_in < -1e6) c_in = -1e6;
+    if (c_in > 1e6) c_in = 1e6;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const double o = __shfl_up_sync(0xffffffffu, c_in, off);

@@ -17,7 +17,8 @@
 namespace gdr {
 
 constexpr int kShortConvMax = 8;
-constexpr int kConvMaxT = 0x7fffffff - 1024;  // token counters run past T by a run and the groups read ahead
+constexpr int kConvMax = 0x7fffffff - 1024;  // of T and C: token counters run past T by a run and the groups read ahead,
+                                              // channels past C by a warp's
 
 struct ConvArgs {
     int B, T, C, ldx, silu, run, runs;  // token stride of x; tokens per run, runs per sequence

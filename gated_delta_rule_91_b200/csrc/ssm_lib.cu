@@ -90,7 +90,7 @@ gdr_status check_conv(const char *fn, int B, int T, int C, int K, gdr_dtype dt, 
     if (K < 1 || K > kShortConvMax)
         return fail(GDR_ERR_UNSUPPORTED, "%s: conv width K=%d (supported: 1..%d)", fn, K, kShortConvMax);
     if ((long long)B * T * C >= (1LL << 31)) return fail(GDR_ERR_UNSUPPORTED, "%s: B*T*C exceeds 2^31-1", fn);
-    if (T > kConvMaxT) return fail(GDR_ERR_UNSUPPORTED, "%s: T=%d (at most %d)", fn, T, kConvMaxT);
+    if (T > kConvMax || C > kConvMax) return fail(GDR_ERR_UNSUPPORTED, "%s: T=%d C=%d (at most %d)", fn, T, C, kConvMax);
     if (*ldx == 0) *ldx = C;
     if (*ldx < C) return fail(GDR_ERR_INVALID_ARGUMENT, "%s: token stride ldx=%d is less than C=%d", fn, *ldx, C);
     return GDR_OK;

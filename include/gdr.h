@@ -491,7 +491,7 @@ GDR_API gdr_status gdr_ssm_step(int B, int H, int G, int P, int N, gdr_dtype dt,
  *        NULL): the last K-1 inputs, for the next segment or token.  It may
  *        equal conv_state_in.  A decode token is the call with T = 1.
  *   Supported: K in 1..8, any C >= 1 (16-byte vectors where C and ldx allow
- *   them), B*T*C < 2^31, T < 2^31 - 1024.  Both states are ignored when K = 1.
+ *   them), B*T*C < 2^31, T and C < 2^31 - 1024.  Both states are ignored when K = 1.
  */
 GDR_API gdr_status gdr_conv_fwd(int B, int T, int C, int K, gdr_dtype dt, int silu, const void *x, int ldx,
                         const float *w, const float *bias, const void *conv_state_in,

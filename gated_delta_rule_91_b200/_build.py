@@ -38,7 +38,11 @@ def _sources(unit):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the units that are older than their sources and link libgdr.so."""
+    """Compile the units that are older than their sources and link libgdr.so; nothing where it is newer than them all."""
+    if not force and os.path.exists(LIB):
+        t = os.path.getmtime(LIB)
+        if all(os.path.getmtime(s) <= t for unit in UNITS for s in _sources(unit)):
+            return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     pid = os.getpid()
     running, objects = [], []

@@ -1,5 +1,5 @@
-// common.cuh -- internals shared by the kernels of libgdr.so (one translation
-// unit: gdr_lib.cu includes every kernel header after this one).
+// common.cuh -- internals shared by the kernels of libgdr.so, whose two
+// translation units (gdr_lib.cu and ssm_lib.cu) include it first.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -17,8 +17,8 @@ namespace gdr {
 constexpr int kChunk = 64;
 
 // Device status word: kernels whose waits are bounded record
-// GDR_ERR_TIMEOUT here instead of spinning forever; gdr_check_status() reads
-// and clears it.
+// GDR_ERR_TIMEOUT here instead of spinning forever.  Each translation unit has
+// its own; gdr_check_status() reads and clears both.
 __device__ int g_status;
 
 __device__ __forceinline__ void record_status(int code) { atomicCAS(&g_status, 0, code); }

@@ -6,9 +6,11 @@
 // neighbouring channels (8 bytes of bf16: with 8 its windows leave one block a
 // SM) and walks a run of tokens with the last K-1 inputs in registers, so that
 // only the K-1 inputs before a run are read a second time, from L2.  B=4 T=4096
-// C=2304 K=4 bf16: forward 35 us (4.3 TB/s; 14 warp instructions an element, two
+// C=2304 K=4 bf16, calls back to back (as all times here unless they say cold):
+// forward 35 us (4.3 TB/s; 14 warp instructions an element, two
 // of them exponential and reciprocal: half of all issue slots and 55 % of that
-// unit's at 24 warps a SM), backward 57 us (4.0 TB/s; 12 warps a SM, since its
+// unit's at 24 warps a SM, for which 36 bytes a thread spill, 84 of fp32),
+// backward 57 us (4.0 TB/s; 12 warps a SM, since its
 // two windows, the taps and their sums take 165 registers: held to 128 it spilled
 // and lost 4 us, held to 96 it took 151 us).
 #pragma once
@@ -510,7 +512,7 @@ inline int conv_fwd_run(int B, int T, int C, int K, int V, bool f32, int fit) {
     const int most = f32 && K <= 4 ? 40 : 160;
     long long best = -1;
     int at = 8;
-    for (int run = 8; run <= most; run += 8) {
+    for (int run = 8; run <= most && run < T + 8; run += 8) {
         const long long blocks = (cols * ((T + run - 1) / run) * B + 7) / 8;
         const long long cost = (blocks + fit - 1) / fit * ((run < T ? run : T) + 8);
         if (best < 0 || cost < best) {
@@ -521,8 +523,9 @@ inline int conv_fwd_run(int B, int T, int C, int K, int V, bool f32, int fit) {
     return at;
 }
 // The backward is one launch that fits (slots x columns, three blocks an SM up to K = 4); a warp's runs are as long as
-// their number stays the same for every warp and no run passes 192 tokens.  C=2304 K=4 bf16: B=4 T=4096 61 us (172;
-// 64, 2.7 runs a warp: 70), T=65536 199 us (172; 64: 219), T=512 18 us (16; 64: 23).
+// their number stays the same for every warp and no run passes 192 tokens.  C=2304 K=4 bf16: B=4 T=4096 58 us (172;
+// 64, 2.7 runs a warp: 66, 192: 62), T=6000 82 us (128; 64: 86, 172: 88), T=65536 at B=1 194 us (64: 215), T=512 19 us (20; 32:
+// 17, 64: 19, 128: 27).
 struct ConvPlan {
     int run, slots;
 };

@@ -7,9 +7,9 @@
 // HBM-bound: every row is read once into registers (raw, as stored) and both
 // statistics are taken from there, the variance from centred values.  TPR
 // threads share a row and hold NV vectors of V elements each.  16384 x 2048
-// bf16 with the residual stream: forward 47 us (5.7 TB/s), backward 68 us (3.9
+// bf16 with the residual stream, calls back to back: forward 47 us (5.7 TB/s), backward 68 us (3.9
 // TB/s: rows at 16 warps a SM, bound by their exchanges and half of all issue
-// slots, and 7 us for the sum of the blocks' partial rows).
+// slots, and 4 us for the sum of the blocks' partial rows).
 #pragma once
 #include "common.cuh"
 #include "conv.cuh"
@@ -80,7 +80,7 @@ __device__ __forceinline__ void norm_reduce(float (&s)[NS], float *buf) {
 }
 
 // The backward's row over two to four warps takes one barrier: each warp centres its values on its own mean, and the sums
-// are then moved to the row's (sum (h - m)^2 = sum (h - m_w)^2 + n_w (m_w - m)^2).  At 16384 x 2048 bf16 77 us, 84 with a
+// are then moved to the row's (sum (h - m)^2 = sum (h - m_w)^2 + n_w (m_w - m)^2).  At 16384 x 2048 bf16 and cold caches 77 us, 84 with a
 // barrier for the mean and one for the sums; over 8 and 16 warps every thread's joining of them costs more than the
 // barrier (16384 x 4096: 152 us against 135), and so does the forward's.
 __device__ __forceinline__ float norm_warp_sum(float x) {
@@ -421,7 +421,10 @@ constexpr int kNormBwdMaxBlocks = 148 * 8;
 // Calls F<V, TPR, NV, NT>: vectors of 16 bytes where D allows, else single elements.  The fewest threads per row
 // that hold it in at most 16 elements a thread, a warp where that is enough: a thread's exchanges with the others are
 // then spread over 16 elements, and the backward's five arrays of them still fit its registers (single elements are half
-// a pair each, so 4 of them: 18304 x 1333 fp32 took 369 us with 8, in blocks of 512 threads that spilled).
+// a pair each, so 4 of them: 18304 x 1333 fp32 takes 194 us, and took 369 with 8, in blocks of 512 threads that spilled).
+// Wider rows have more elements a thread than the backward's registers hold: vectors above 8192 columns spill 484 (bf16) and
+// 644 bytes a thread (4096 x 16384 bf16: 199 us, 2.7 TB/s), single elements above 2048 columns 170 to 2400 (8192 x 3001 fp32:
+// 235 us, 1.7 TB/s).
 template <typename T, bool BWD, template <typename, int, int, int, int> class F, typename... A>
 cudaError_t norm_pick(int D, A... args) {
     constexpr int V = sizeof(T) == 2 ? 8 : 4, M = 16, S = BWD ? 4 : 16;

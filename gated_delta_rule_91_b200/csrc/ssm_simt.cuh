@@ -10,7 +10,7 @@
 // operands from shared memory: a thread's 4 x 4..8 tile is read as vectors
 // along both tile axes, so every product's operands are stored with the
 // summed index outermost.  fp32 B=3 T=777 H=6 P=N=64: 42 us; gradients of B=2 T=333
-// H=4 P=128 N=64: 76 us (latency: 48 to 234 blocks of one to three a SM).
+// H=4 P=128 N=64: 72 us, 38 of them the chunks' gradients (latency: 48 to 234 blocks of one to three a SM).
 #pragma once
 #include "launch.cuh"
 #include "ssm_common.cuh"
@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_y_simt_kernel(SsmArgs a, cons
 //     d log a_t = sum_{i >= t > j} R_ij Delta_j + sum_{i >= t} e^{c_i} dy_i.S_in C_i
 //                 + sum_{j < t} Delta_j e^{c_last - c_j} x_j.G B_j + e^{c_last} <G, S_in>
 // The double sum of d log a_t is the difference of the prefix sums of the
-// columns and rows of strict pairs, which starts at exactly 0.
+// columns and rows of strict pairs, which starts at exactly 0.  Both are sums in
+// 64 bits of the same R_ij (times Delta_j, exact there): in 32 bits they round
+// apart, and the remainder stays in every later token's difference (dA was up to
+// 5.5e-6 off, 2e-7 now).
 // part[0..2][b*nch+ch][h]: this chunk's sums for dA, d(delta_bias), dD.
 __device__ __forceinline__ void ssm_token_grads(const SsmArgs &a, int b, int h, int t0, int valid, int Q, const float *s_dt,
                                                 const double *colU, const float *diag, const double *row, const float *gx,

@@ -181,9 +181,10 @@ __device__ __forceinline__ void ssm_enter_segment(float (&v)[W], const float *se
 // OUT: from the state that enters the segment, every chunk's entering state is written to out_S or out_G (fp32,
 // [unit][P / 4][N][4], unit = (b, chunk, head): a warp writes 512 bytes at once), and dS0 at the end.  Otherwise: from
 // zero, the segment's own sum goes to seg_S or seg_G [b][seg][h][P][N], and its decay to dec.
-// Two or three stages of operands: while a chunk's products run, the next chunk's rows are weighted (without states to
-// write a chunk takes about 3900 cycles at P = N = 128; with one stage and half the warps it took 4500, and 9400 with
-// states stored row by row against 5600 now).  What bounds it is the operands' way from L2: 64 KB a chunk and SM.
+// Two or three stages of operands: while a chunk's products run, the next chunk's rows are weighted.  At P = N = 128 the
+// segments' sums of 16 chunks take 50 us (B=4 T=4096 H=16: 41 with two parts) and the states of 32 chunks 129 us (109 with
+// two parts, whose states left as bf16 through shared memory; states stored row by row took 9400 cycles a chunk against 5600
+// then).  What bounds it is the operands' way from L2, 64 KB a chunk and SM, and the states' to memory.
 template <int P, int N>
 struct SsmWalkTc {
     static constexpr int kThreads = 512, PW = P / 4;

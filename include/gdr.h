@@ -429,6 +429,8 @@ GDR_API gdr_status gdr_seg_fixup(int B, int T, int H, int dk, int dv, gdr_dtype 
  *   accuracy (operands of the tensor cores that are not bf16 themselves are
  *   split into bf16 parts): fp32 outputs are as exact as fp32 operations, bf16
  *   outputs one rounding away from that.
+ *   GDR_SSM_KERNEL=simt in the environment runs bf16 inputs on the CUDA cores
+ *   instead (slower; the workspace sizes follow it).
  *   An output at the address of an input (S_T = S0, y = x) is refused, here and
  *   in the scan's and the convolution's other calls.
  */

@@ -18,7 +18,7 @@
 // where fp32 results follow from the product and G_out as two for dx.  The double sums of R = L K W are taken on CUDA
 // cores from the fp32 accumulators.  With one part for M', dK and dx's G_out, and the states kept as two, dx, dB and dC
 // were 2.3e-3 off 64 bits (one rounding: 1.7e-3), dS0 2.5e-6 and dA and the bias's gradient up to 1e-5; now 1e-7 to 4e-7.
-// B=4 T=4096 H=16 P=N=128: 443 us (walk 130, gradients 300), 308 with the fewer parts.
+// B=4 T=4096 H=16 P=N=128: 440 us (walk 129, gradients 301), 308 with the fewer parts.
 #pragma once
 #include "ssm_tc.cuh"
 
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ssm_tc_grad_kernel(
 
 // ---- host side ------------------------------------------------------------------------------
 // CTAs per group of heads: a CTA costs about half a head's time beside its heads (the first loads, dB and dC), and with
-// several of them partial sums in fp32 and a launch that adds them.  Measured: B=4 T=4096 H=16 P=N=128, one CTA 441 us (two:
+// several of them partial sums in fp32 and a launch that adds them.  Measured: B=4 T=4096 H=16 P=N=128, one CTA 440 us (two:
 // 466); B=1 T=4096, four 174 us (eight: 188, two: 241); B=2 T=1024 H=4 G=2 P=64, two 62 us (one: 70).
 inline int ssm_grad_splits(int B, int T, int H, int G) {
     const int nch = (T + kTcQ - 1) / kTcQ, HG = H / G, sms = sm_count();
@@ -670,7 +670,7 @@ inline int ssm_grad_splits(int B, int T, int H, int G) {
 
 // Chunks per segment of the walk: rounds of chunks over the SMs (one CTA each, both directions); a cut costs the
 // segments' own sums first (a chunk there about 0.8 of one with its states written) and one to three launches.  Measured:
-// B=4 T=4096 H=16 P=N=128, uncut 441 us (2 segments: 545); B=1 T=4096, 4 segments 173 us (1: 231, 8: 189); B=1 T=2048 H=8 P=64,
+// B=4 T=4096 H=16 P=N=128, uncut 440 us (2 segments: 545); B=1 T=4096, 4 segments 173 us (1: 231, 8: 189); B=1 T=2048 H=8 P=64,
 // 8 segments 66 us (1: 85, 4: 72, 16: 78).
 inline int ssm_walk_chunks(int B, int T, int H) {
     const int nch = (T + kTcQ - 1) / kTcQ, sms = sm_count();

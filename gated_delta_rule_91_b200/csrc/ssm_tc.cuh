@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(128) ssm_gate_kernel(SsmArgs a, float *__restr
 
 // ---- 1. walks over the chunks ------------------------------------------------------------
 // Up to this many segments are joined by every reader itself (it reads the sums of the segments before its own);
-// ssm_scan_kernel joins more.  B=4 T=4096 H=16 P=N=128, 2 segments: 175 us, with the scan's launch 183 us; B=1, 8
+// ssm_scan_kernel joins more.  B=4 T=4096 H=16 P=N=128, 2 segments: 173 us, with the scan's launch 182 us; B=1, 8
 // segments: 58 us and 60 us.
 constexpr int kJoinMost = 8;
 
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(SsmYTc<P, N, LO>::NT, P == 64 && !LO ? 2 : 1) 
 // ---- host side ------------------------------------------------------------------------------
 // Chunks per segment.  In units of a chunk of the output kernel: whole rounds of CTAs over the SMs, where two CTAs of P =
 // 64 on an SM take 1.5 of one's time; a cut costs the walk over the segments first (about half of that) and two
-// launches.  Measured: B=4 T=4096 H=16 P=N=128, 2 segments 175 us (1: 249, 3: 228); B=1 T=4096, 8 segments 58 us (6: 73, 16:
+// launches.  Measured: B=4 T=4096 H=16 P=N=128, 2 segments 173 us (1: 249, 3: 228); B=1 T=4096, 8 segments 58 us (6: 73, 16:
 // 65); B=8 T=2048 H=16 P=64, uncut 107 us (2 segments: 117); B=1 T=65536 P=64, 37 segments 376 us (16: 404, 32: 411); B=2
 // T=2048 H=24 P=64, 6 segments 55 us (3: 64, 8: 69).
 inline int ssm_tc_chunks(int B, int T, int H, int P) {
